@@ -17,6 +17,7 @@ Per-token tensors are ``[B, T, H, d]``; states ``[B, H, dk, dv]`` float32.
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 
 import torch
@@ -24,7 +25,8 @@ import torch
 __all__ = [
     "MuirError", "lib", "chunk_fwd", "chunk_bwd", "chunk_fwd_varlen", "chunk_bwd_varlen",
     "recurrent_step", "qk_prologue", "chunk_fwd_fused", "chunk_bwd_fused", "MuirFusion",
-    "qk_prologue_bwd", "fwd_workspace_bytes", "bwd_workspace_bytes", "MuirChunkFunction",
+    "qk_prologue_bwd", "rotary", "rotary_frequencies", "kv_cache", "kv_append", "attn_step",
+    "fwd_workspace_bytes", "bwd_workspace_bytes", "MuirChunkFunction",
     "LIB_PATH",
 ]
 
@@ -61,6 +63,14 @@ class MuirFusion(ctypes.Structure):
 class MuirFusionGrads(ctypes.Structure):
     _fields_ = [("dlatent", ctypes.c_void_p), ("dU", ctypes.c_void_p * 5),
                 ("dbias", ctypes.c_void_p * 5)]
+
+
+class MuirKvCache(ctypes.Structure):
+    _fields_ = [("Hk", ctypes.c_int), ("d", ctypes.c_int), ("page", ctypes.c_int),
+                ("num_pages", ctypes.c_int), ("max_pages", ctypes.c_int),
+                ("k_pages", ctypes.c_void_p), ("v_pages", ctypes.c_void_p),
+                ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p),
+                ("table", ctypes.c_void_p)]
 
 
 # gate families of the fused projection, in the latent's column order
@@ -117,6 +127,15 @@ def lib():
         L.muir_chunk_bwd_fused.restype = I
         L.muir_chunk_fwd_noalloc.argtypes = [SP] + [P] * 10 + [P]
         L.muir_chunk_fwd_noalloc.restype = I
+        LL, F, CP = ctypes.c_longlong, ctypes.c_float, ctypes.POINTER(MuirKvCache)
+        L.muir_rotary.argtypes = [I] * 7 + [P, LL, P, LL, P, P, F, I, I, P, LL, P, LL, P]
+        L.muir_rotary.restype = I
+        L.muir_kv_append.argtypes = [I, I, I, P, LL, P, LL, CP, P, P, P]
+        L.muir_kv_append.restype = I
+        L.muir_attn_step_workspace.argtypes = [I, I, CP]
+        L.muir_attn_step_workspace.restype = S
+        L.muir_attn_step.argtypes = [I, I, CP, P, P, F, I, P, P, S, P]
+        L.muir_attn_step.restype = I
         L.muir_profile_enable.argtypes = [I]
         L.muir_profile_enable.restype = None
         L.muir_profile_reset.argtypes = []
@@ -456,6 +475,193 @@ def qk_prologue_bwd(x, dy, out=None):
                                 _stream(x.device))
     _check("muir_qk_prologue_bwd", rc)
     return out
+
+
+# ------------------------------------------------------------------ softmax-attention layers
+
+
+def _dev_call(name, t, *args):
+    """Calls ``name`` with the current stream of ``t``'s device, that device current."""
+    fn = getattr(lib(), name)
+    dev = t.device.index
+    stream = torch.cuda.current_stream(dev).cuda_stream
+    if dev == torch.cuda.current_device():
+        rc = fn(*args, stream)
+    else:
+        with torch.cuda.device(dev):
+            rc = fn(*args, stream)
+    if rc != 0:
+        raise MuirError(name, rc)
+
+
+def _rows(t, name, dev=None):
+    """Address and token stride of a ``[B, T, H, d]`` tensor whose heads are dense within a
+    token and whose tokens are evenly spaced (a part of a packed projection qualifies)."""
+    B, T, H, d = t.shape
+    sb, st, sh, sd = t.stride()
+    if not t.is_cuda:
+        raise ValueError("libmuir takes CUDA tensors only")
+    if dev is not None and t.device != dev:
+        raise ValueError(f"{name} is on {t.device}, not on {dev}")
+    if (sd != 1 and d > 1) or (sh != d and H > 1):
+        raise ValueError(f"{name}: channels and heads of a token must be dense")
+    if T == 1 and B > 1:
+        st = sb
+    elif T <= 1 or B * T == 0:
+        st = H * d
+    elif B > 1 and sb != T * st:
+        raise ValueError(f"{name}: tokens must be evenly spaced")
+    return t.data_ptr(), st
+
+
+def _same(t, name, shape, dtype, dev):
+    """Address of a contiguous tensor of exactly this shape, type and device."""
+    if t is None:
+        return None
+    if tuple(t.shape) != tuple(shape) or t.dtype != dtype or t.device != dev or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {dev}")
+    return t.data_ptr()
+
+
+def rotary_frequencies(rot, base=10000.0, scaling=None, factor=1.0, original_length=2048,
+                       beta_fast=32.0, beta_slow=1.0, device="cuda"):
+    """``(inv_freq, mscale)`` for :func:`rotary`: radians per position of the ``rot // 2``
+    pairs (float64 on ``device``) and the factor on the rotated values.
+
+    ``scaling`` stretches them for contexts ``factor`` times ``original_length``: ``"linear"``
+    divides every frequency by ``factor``; ``"ntk"`` raises the base so that the slowest
+    pair slows down by ``factor`` and the fastest keeps its speed; ``"yarn"`` (arXiv
+    2309.00071) keeps pairs that turn more than ``beta_fast`` times within the original
+    length, divides those that turn fewer than ``beta_slow`` times by ``factor``, blends
+    between, and scales the values by ``0.1 ln(factor) + 1``."""
+    if rot < 2 or rot % 2:
+        raise ValueError("rot must be a positive even number")
+    if scaling not in (None, "linear", "ntk", "yarn"):
+        raise ValueError(f"unknown scaling {scaling!r}")
+    if not (base > 1.0 and factor > 0.0):
+        raise ValueError("base must exceed 1 and factor 0")
+    mscale = 1.0
+    if scaling == "ntk" and rot > 2:
+        base = base * factor ** (rot / (rot - 2))
+    f = base ** (-torch.arange(0, rot, 2, dtype=torch.float64) / rot)
+    if scaling == "linear":
+        f = f / factor
+    elif scaling == "yarn":
+        def pair_with(turns):
+            return rot * math.log(original_length / (turns * 2 * math.pi)) / (2 * math.log(base))
+        low = max(math.floor(pair_with(beta_fast)), 0)
+        high = min(math.ceil(pair_with(beta_slow)), rot - 1)
+        ramp = ((torch.arange(rot // 2, dtype=torch.float64) - low) / max(high - low, 0.001)).clamp(0, 1)
+        f = f / factor * ramp + f * (1 - ramp)
+        mscale = 0.1 * math.log(factor) + 1.0 if factor > 1.0 else 1.0
+    return f.to(device), mscale
+
+
+def rotary(q, k=None, positions=None, inv_freq=None, interleaved=False, mscale=1.0,
+           inverse=False, q_out=None, k_out=None):
+    """Rotary positions (``muir_rotary``) of ``q [B, T, Hq, d]`` and, in the same launch,
+    ``k [B, T, Hk, d]`` (bfloat16 or float32; parts of a packed projection are taken as they
+    lie).  ``positions`` is int32 ``[B, T]`` (None: 0 .. T-1), ``inv_freq`` float64
+    ``[rot / 2]`` (see :func:`rotary_frequencies`) and fixes the rotated channels.
+    ``inverse`` applies the transpose, which maps an output gradient to the input's.
+    ``q_out`` / ``k_out`` may be the inputs (in place).  Returns ``(q_out, k_out)``, or
+    ``q_out`` alone without ``k``."""
+    B, T, Hq, d = q.shape
+    dev = q.device
+    dt = _dt(q)
+    if inv_freq is None:
+        raise ValueError("inv_freq is required (rotary_frequencies makes it)")
+    if q_out is None:
+        q_out = torch.empty(B, T, Hq, d, dtype=q.dtype, device=dev)
+    qp, ql = _rows(q, "q")
+    op, ol = _rows(q_out, "q_out", dev)
+    Hk, kp, kl, kop, kol = 0, None, 0, None, 0
+    if k is not None:
+        if k.shape[:2] != q.shape[:2] or k.shape[3] != d or k.dtype != q.dtype:
+            raise ValueError("k must have q's batch, tokens, channels and dtype")
+        Hk = k.shape[2]
+        if k_out is None:
+            k_out = torch.empty(B, T, Hk, d, dtype=k.dtype, device=dev)
+        kp, kl = _rows(k, "k", dev)
+        kop, kol = _rows(k_out, "k_out", dev)
+        if k_out.shape != k.shape or k_out.dtype != k.dtype:
+            raise ValueError("k_out must have k's shape and dtype")
+    elif k_out is not None:
+        raise ValueError("k_out without k")
+    if q_out.shape != q.shape or q_out.dtype != q.dtype:
+        raise ValueError("q_out must have q's shape and dtype")
+    rot = 2 * inv_freq.numel()
+    _dev_call("muir_rotary", q, B, T, Hq, Hk, d, rot, dt, qp, ql, kp, kl,
+              _same(positions, "positions", (B, T), torch.int32, dev),
+              _same(inv_freq, "inv_freq", (rot // 2,), torch.float64, dev), mscale,
+              int(bool(interleaved)), int(bool(inverse)), op, ol, kop, kol)
+    return q_out if k is None else (q_out, k_out)
+
+
+def kv_cache(num_pages, Hk, page, d, device="cuda"):
+    """Fresh cache tensors ``(k_pages, v_pages, k_scale, v_scale)``: float8_e4m3fn codes
+    ``[num_pages, Hk, page, d]`` and float32 scales ``[num_pages, Hk]``."""
+    z = [torch.zeros(num_pages, Hk, page, d, dtype=torch.uint8, device=device).view(torch.float8_e4m3fn)
+         for _ in range(2)]
+    return z[0], z[1], *[torch.ones(num_pages, Hk, dtype=torch.float32, device=device) for _ in range(2)]
+
+
+def _cache(k_pages, v_pages, k_scale, v_scale, page_table, B, dev):
+    num, Hk, page, d = k_pages.shape
+    shape = (num, Hk, page, d)
+    if page_table.dim() != 2 or page_table.shape[0] != B:
+        raise ValueError("page_table must be [B, max_pages]")
+    return MuirKvCache(
+        Hk, d, page, num, page_table.shape[1],
+        _same(k_pages, "k_pages", shape, torch.float8_e4m3fn, dev),
+        _same(v_pages, "v_pages", shape, torch.float8_e4m3fn, dev),
+        _same(k_scale, "k_scale", (num, Hk), torch.float32, dev),
+        _same(v_scale, "v_scale", (num, Hk), torch.float32, dev),
+        _same(page_table, "page_table", (B, page_table.shape[1]), torch.int32, dev))
+
+
+def kv_append(k, v, k_pages, v_pages, k_scale, v_scale, page_table, start, count=None):
+    """Writes the tokens of ``k, v [B, T, Hk, d]`` (bfloat16 or float32) into the cache
+    (:func:`kv_cache`), in place (``muir_kv_append``): token t of sequence b to position
+    ``start[b] + t`` for t below ``count[b]`` (None: T).  ``page_table`` is int32
+    ``[B, max_pages]``, ``start`` and ``count`` int32 ``[B]``, all on the device."""
+    B, T, Hk, d = k.shape
+    dev = k.device
+    dt = _dt(k)
+    if v.shape != k.shape or v.dtype != k.dtype:
+        raise ValueError("v must have k's shape and dtype")
+    if tuple(k_pages.shape[i] for i in (1, 3)) != (Hk, d):
+        raise ValueError("the cache's heads and channels must be k's")
+    c = _cache(k_pages, v_pages, k_scale, v_scale, page_table, B, dev)
+    kp, kl = _rows(k, "k")
+    vp, vl = _rows(v, "v", dev)
+    _dev_call("muir_kv_append", k, B, T, dt, kp, kl, vp, vl, ctypes.byref(c),
+              _same(start, "start", (B,), torch.int32, dev),
+              _same(count, "count", (B,), torch.int32, dev))
+
+
+def attn_step(q, k_pages, v_pages, k_scale, v_scale, page_table, lens, scale=None, window=0,
+              o=None, ws=None):
+    """One bfloat16 query token ``q [B, Hq, d]`` of every sequence attends over its first
+    ``lens[b]`` cached tokens, or the last ``window`` of them (``muir_attn_step``).
+    ``scale`` defaults to ``d ** -0.5``.  Returns ``o [B, Hq, d]``."""
+    B, Hq, d = q.shape
+    dev = q.device
+    if k_pages.shape[3] != d:
+        raise ValueError("the cache's channels must be q's")
+    qp = _same(q, "q", (B, Hq, d), torch.bfloat16, dev)
+    if not q.is_cuda:
+        raise ValueError("libmuir takes CUDA tensors only")
+    c = _cache(k_pages, v_pages, k_scale, v_scale, page_table, B, dev)
+    if o is None:
+        o = torch.empty_like(q)
+    op = _same(o, "o", (B, Hq, d), torch.bfloat16, dev)
+    need = lib().muir_attn_step_workspace(B, Hq, ctypes.byref(c))
+    wsb = _workspace(need, dev, ws)
+    _dev_call("muir_attn_step", q, B, Hq, ctypes.byref(c), qp,
+              _same(lens, "lens", (B,), torch.int32, dev), d ** -0.5 if scale is None else scale,
+              window, op, None if wsb is None else wsb.data_ptr(), 0 if wsb is None else wsb.numel())
+    return o
 
 
 class MuirChunkFunction(torch.autograd.Function):

@@ -4,6 +4,7 @@
 #include <stdint.h>
 
 #include "../../include/muir.h"
+#include "checks.h"
 #include "chunk_units.h"
 #include "bwd2.h"
 #include "fwd2.h"
@@ -11,37 +12,6 @@
 #include "kernels.h"
 
 namespace {
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-#ifdef MUIR_DEBUG
-// Debug builds (build.py --debug) also ask the CUDA runtime where each
-// pointer lives and refuse host memory the device cannot address.
-bool device_addressable(const void* p) {
-    cudaPointerAttributes a;
-    if (cudaPointerGetAttributes(&a, p) != cudaSuccess) {
-        cudaGetLastError();
-        return false;
-    }
-    return a.type == cudaMemoryTypeDevice || a.type == cudaMemoryTypeManaged ||
-           (a.type == cudaMemoryTypeHost && a.devicePointer != nullptr);
-}
-bool ok_ptr(const void* p) { return p != nullptr && aligned16(p) && device_addressable(p); }
-bool ok_opt(const void* p) { return p == nullptr || (aligned16(p) && device_addressable(p)); }
-#else
-bool ok_ptr(const void* p) { return p != nullptr && aligned16(p); }
-bool ok_opt(const void* p) { return p == nullptr || aligned16(p); }
-#endif
-bool ok_dtype(muir_dtype d) { return d == MUIR_BF16 || d == MUIR_FP32; }
-
-// The kernels use sm_100a instructions: require compute capability 10.x.
-muir_status check_device() {
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) return MUIR_ERR_CUDA;
-    int major = 0;
-    if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess)
-        return MUIR_ERR_CUDA;
-    return major == 10 ? MUIR_OK : MUIR_ERR_UNSUPPORTED;
-}
 
 // Shape checks shared by the chunk entry points (no CUDA calls).
 muir_status check_shape(const muir_shape* s) {
@@ -99,12 +69,6 @@ const void* at_row(const void* p, long long row, size_t row_bytes) {
     return static_cast<const char*>(p) + (size_t)row * row_bytes;
 }
 
-muir_status from_cuda(cudaError_t err) {
-    if (err == cudaSuccess) return MUIR_OK;
-    if (err == cudaErrorNotSupported) return MUIR_ERR_UNSUPPORTED;
-    return MUIR_ERR_CUDA;
-}
-
 }  // namespace
 
 extern "C" {
@@ -126,7 +90,8 @@ muir_status muir_device_wait_status(void) {
     const unsigned int n = muir::timeouts_bf16_d128() + muir::timeouts_bf16_d64() +
                            muir::timeouts_f32_d128() + muir::timeouts_f32_d64() +
                            muir::v2::timeouts_v2() + muir::v2::timeouts_bwd2() +
-                           muir::timeouts_selftest() + muir::v2::timeouts_gates();
+                           muir::timeouts_selftest() + muir::v2::timeouts_gates() +
+                           muir::timeouts_kv();
     return n ? MUIR_ERR_DEVICE_TIMEOUT : MUIR_OK;
 }
 

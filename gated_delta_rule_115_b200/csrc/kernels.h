@@ -1,6 +1,7 @@
 // kernels.h -- internal launchers of libmuir (not part of the C ABI).
 #pragma once
 
+#include <cuda.h>
 #include <cuda_runtime.h>
 #include <stddef.h>
 
@@ -14,6 +15,49 @@ cudaError_t launch_decode(int B, int H, int D, bool in_bf16, bool out_bf16, cons
 // q/k feature prologue y = SiLU(x) / ||SiLU(x)|| per row of d (bwd: dx from x, dy).
 cudaError_t launch_qk_prologue(long long rows, int d, bool bf16, const void* x, const void* dy,
                                void* out, bool bwd, cudaStream_t st);
+
+// Rotary positions (rotary.cu).  Leading dimensions are elements between tokens.
+struct RotaryArgs {
+    const void *q, *k;              // k may be null with Hk = 0
+    void *q_out, *k_out;
+    long long q_ld, k_ld, qo_ld, ko_ld;
+    const int* positions;           // [tokens], or null: the token's index in its sequence
+    const double* inv_freq;         // [rot / 2]
+    float mscale;
+    int T, Hq, Hk, d, rot;
+    bool inverse;
+    long long tokens;               // B * T
+    int tokens_per_block;           // set by the launcher
+};
+cudaError_t launch_rotary(RotaryArgs a, bool bf16, bool interleaved, cudaStream_t st);
+
+// The paged 8-bit key/value cache (kvcache.cu).
+struct AppendArgs {
+    const void *k, *v;              // [B][T][Hk][d]
+    long long k_ld, v_ld;           // elements between tokens
+    void *k_pages, *v_pages;        // e4m3 codes [num_pages][Hk][page][d]
+    float *k_scale, *v_scale;       // [num_pages][Hk]
+    const int *table, *start, *count;  // [B][max_pages], [B], [B] or null
+    int T, Hk, page, num_pages, max_pages;
+};
+cudaError_t launch_kv_append(const AppendArgs& a, int B, int d, bool bf16, cudaStream_t st);
+
+struct StepArgs {
+    CUtensorMap tk, tv;             // set by the launcher
+    const void* q;                  // [B][Hq][d] bf16
+    const void *k_pages, *v_pages;
+    const float *k_scale, *v_scale;
+    const int *table, *lens;
+    void* o;                        // [B][Hq][d] bf16
+    float scale_log2;               // softmax scale * log2(e)
+    int window;
+    int Hq, Hk, page, num_pages, max_pages;
+    int splits, min_keys;           // set by the launcher, with the workspace's parts
+    float *part, *part_lse;         // [B * Hq][splits][d], [B * Hq][splits]
+};
+size_t attn_step_ws_bytes(int B, int Hq, int Hk, int d, int page, int max_pages);
+cudaError_t launch_attn_step(StepArgs a, int B, int d, void* ws, cudaStream_t st);
+unsigned int timeouts_kv();
 
 // Problem description shared by the chunk kernels.
 struct ChunkProblem {

@@ -1,0 +1,625 @@
+// kvcache.cu -- the paged 8-bit key/value cache of an attention layer: appending
+// tokens, and one query token per sequence attending over it.
+//
+// A page holds `page` tokens of every key head: codes [Hk][page][d] in e4m3 and one
+// float32 scale for each (page, head), value = code * scale.  Scales are powers of
+// two: e4m3 carries its own exponent, so a finer scale buys no precision, and a page
+// whose scale has to grow when a larger token arrives is encoded again exactly (only
+// codes that become subnormal lose bits).
+//
+//   append:  scale = max(scale held, smallest 2^e >= 2^-100 with amax / 2^e <= 448)
+//            code  = e4m3(x / scale), round to nearest even
+//   step:    s_j = scale_q k_j.q;  o = sum_j exp(s_j - max) v_j / sum_j exp(s_j - max)
+//
+// Both are bound by HBM.  The step reads 2 d bytes a key and head and nothing else of
+// that size; see k_attn_step for how the codes reach the tensor cores.
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+
+#include "common.cuh"
+#include "kernels.h"
+#include "profile.h"
+#include "tc2.cuh"
+#include "tmap.h"
+
+namespace muir {
+
+__device__ unsigned int g_kv_timeouts;
+
+namespace {
+
+constexpr int kAppThreads = 128;
+
+__device__ __forceinline__ void kv_unpack(const uint4& a, float* v, float) {
+    v[0] = __uint_as_float(a.x); v[1] = __uint_as_float(a.y);
+    v[2] = __uint_as_float(a.z); v[3] = __uint_as_float(a.w);
+}
+__device__ __forceinline__ void kv_unpack(const uint4& a, float* v, __nv_bfloat16) {
+    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        v[2 * i] = __uint_as_float(w[i] << 16);
+        v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+}
+
+// Two floats -> two e4m3 codes (round to nearest even, saturating; NaN stays NaN).
+__device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
+    return (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E4M3);
+}
+__device__ __forceinline__ float2 from_e4m3x2(uint32_t two) {
+    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)two, __NV_E4M3);
+    return __half22float2(*reinterpret_cast<const __half2*>(&h));
+}
+
+// Smallest power of two s >= 2^kMinScaleExp with amax <= 448 s (448 = 0.875 2^9).
+constexpr int kMinScaleExp = -100;
+__device__ __forceinline__ float scale_for(float amax) {
+    int e;
+    const float m = frexpf(amax, &e);  // amax = m 2^e, m in [0.5, 1); amax = 0: m = e = 0
+    e -= m <= 0.875f ? 9 : 8;
+    if (amax == 0.f || e < kMinScaleExp) e = kMinScaleExp;
+    return ldexpf(1.f, e);
+}
+
+// One block per (page a sequence's new tokens touch, head, keys or values): the new
+// rows' largest finite magnitude, the page's scale, held rows encoded again if the
+// scale grew, new rows encoded.  Rows of the page behind the new tokens stay as they are.
+template <typename T, int D>
+__global__ void __launch_bounds__(kAppThreads) k_kv_append(AppendArgs p) {
+    constexpr int V = 16 / (int)sizeof(T);  // channels per vector
+    constexpr int PER_ROW = D / V;
+    const int b = blockIdx.z >> 1, which = blockIdx.z & 1, h = blockIdx.y;
+    const int start = p.start[b];
+    int count = p.count ? p.count[b] : p.T;
+    count = count < 0 ? 0 : (count > p.T ? p.T : count);
+    if (start < 0 || count == 0) return;
+    const long long slot = (long long)start / p.page + blockIdx.x;
+    // first and one-past-last new token that fall into this page
+    const long long page0 = slot * p.page;
+    const int lo = (int)max(0LL, page0 - start);
+    const int hi = (int)min((long long)count, page0 + p.page - start);
+    if (lo >= hi || slot >= p.max_pages) return;
+    const int id = p.table[(long long)b * p.max_pages + slot];
+    if (id < 0 || id >= p.num_pages) return;
+
+    const T* src = static_cast<const T*>(which ? p.v : p.k) +
+                   ((long long)b * p.T + lo) * (which ? p.v_ld : p.k_ld) + (long long)h * D;
+    const long long ld = which ? p.v_ld : p.k_ld;
+    unsigned char* dst = static_cast<unsigned char*>(which ? p.v_pages : p.k_pages) +
+                         ((long long)id * p.Hk + h) * p.page * D;
+    float* scale = (which ? p.v_scale : p.k_scale) + (long long)id * p.Hk + h;
+    const int held = (int)(start + lo - page0);  // rows of the page before the new ones
+    const int items = (hi - lo) * PER_ROW;
+    const float old = held > 0 ? *scale : 0.f;
+
+    float amax = 0.f;
+    for (int i = threadIdx.x; i < items; i += kAppThreads) {
+        const int r = i / PER_ROW, c = i % PER_ROW;
+        float v[V];
+        kv_unpack(*reinterpret_cast<const uint4*>(src + r * ld + c * V), v, T());
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            const float a = fabsf(v[j]);
+            if (a <= 3.402823466e38f) amax = fmaxf(amax, a);  // false for infinities and NaN
+        }
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+    __shared__ float part[kAppThreads / 32];
+    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = amax;
+    __syncthreads();  // also: every thread has read the old scale
+#pragma unroll
+    for (int w = 0; w < kAppThreads / 32; ++w) amax = fmaxf(amax, part[w]);
+    const float now = fmaxf(old, scale_for(amax));
+    if (threadIdx.x == 0) *scale = now;
+
+    const float inv = 1.f / now;  // exact: a power of two in [2^-120, 2^100]
+    if (old > 0.f && now != old) {
+        const float ratio = old / now;
+        for (int i = threadIdx.x; i < held * (D / 4); i += kAppThreads) {
+            uint32_t* w = reinterpret_cast<uint32_t*>(dst) + i;
+            const uint32_t x = *w;
+            const float2 a = from_e4m3x2(x & 0xffffu), c = from_e4m3x2(x >> 16);
+            *w = e4m3x2(a.x * ratio, a.y * ratio) | (e4m3x2(c.x * ratio, c.y * ratio) << 16);
+        }
+    }
+    for (int i = threadIdx.x; i < items; i += kAppThreads) {
+        const int r = i / PER_ROW, c = i % PER_ROW;
+        float v[V];
+        kv_unpack(*reinterpret_cast<const uint4*>(src + r * ld + c * V), v, T());
+        uint32_t w[V / 4];
+#pragma unroll
+        for (int j = 0; j < V / 4; ++j)
+            w[j] = e4m3x2(v[4 * j] * inv, v[4 * j + 1] * inv) |
+                   (e4m3x2(v[4 * j + 2] * inv, v[4 * j + 3] * inv) << 16);
+        uint32_t* o = reinterpret_cast<uint32_t*>(dst + (long long)(held + r) * D + c * V);
+        if (V == 8)
+            *reinterpret_cast<uint2*>(o) = make_uint2(w[0], w[V / 4 - 1]);
+        else
+            *o = w[0];
+    }
+}
+
+// ------------------------------------------------------------------ step
+
+// Keys and values travel in stages of kStepKeys keys, copied by TMA into a swizzled
+// ring by one warp that runs ahead; four warps take 16 keys of each stage.
+constexpr int kStepKeys = 64;
+constexpr int kStepWarps = 4;              // consumer warps, 16 keys of a stage each
+constexpr int kStepThreads = 32 * (kStepWarps + 1);
+constexpr int kStepStages = 4;
+constexpr int kRows = 16;                  // query rows of an MMA: the heads that share a key head
+
+struct StepMeta {        // per 16 keys of a stage
+    float ks, lv;        // key scale, log2 of the value scale
+    int lo, hi;          // visible keys [lo, hi) of the 16
+};
+
+template <int D>
+struct StepSmem {
+    static constexpr int kTile = kStepKeys * D;               // bytes of K (or V) in a stage
+    static constexpr int kMeta = kStepStages * 2 * kTile;
+    static constexpr int kBars = kMeta + kStepStages * 4 * (int)sizeof(StepMeta);
+    static constexpr int kBytes = kBars + 2 * kStepStages * 8;
+};
+
+__device__ __forceinline__ uint32_t h2_from_e4m3(uint32_t two) {
+    uint32_t r;
+    asm("{\n.reg .b16 lo, hi;\nmov.b32 {lo, hi}, %1;\ncvt.rn.f16x2.e4m3x2 %0, lo;\n}" : "=r"(r) : "r"(two));
+    return r;
+}
+__device__ __forceinline__ uint32_t h2_from_e4m3_hi(uint32_t two) {
+    uint32_t r;
+    asm("{\n.reg .b16 lo, hi;\nmov.b32 {lo, hi}, %1;\ncvt.rn.f16x2.e4m3x2 %0, hi;\n}" : "=r"(r) : "r"(two));
+    return r;
+}
+
+__device__ __forceinline__ void mma_f16_16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
+                                              uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+        "{%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ float ex2(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+__device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(t2::saddr(bar)) : "memory");
+}
+
+// Byte offset of 16-byte chunk c of row r in a stage's tile, as the tensor map's swizzle
+// places it (128-byte rows: chunk ^ row % 8; 64-byte rows: chunk ^ row / 2 % 4).
+template <int D>
+__device__ __forceinline__ uint32_t step_off(int r, int c) {
+    return D == 128 ? (uint32_t)r * 128u + (uint32_t)((c ^ (r & 7)) << 4)
+                    : (uint32_t)r * 64u + (uint32_t)((c ^ ((r >> 1) & 3)) << 4);
+}
+
+// One block: the heads of one key head (16 at a time) of one sequence over one range of
+// its keys.
+//
+// The products run on mma.sync m16n8k16 in fp16 with float32 sums: the rows are the
+// query heads that share the key head (of 16, the rest zero), so a key costs 16 rows
+// whatever the group, and the kernel stays bound by the cache's bytes.  e4m3 codes are
+// exact in fp16.  A product's contraction may run in any order as long as both operands
+// agree: lane (g, c) takes 32 (16 for d = 64) neighbouring bytes of key g for the score
+// product, and 16 (8) neighbouring columns of keys 2c, 2c+1, 2c+8, 2c+9 for the output,
+// so both read shared memory in 16-byte vectors, conflict-free, with no transposition.
+//
+// Query rows are scaled by a power of two to a largest magnitude in [2^13, 2^14): fp16
+// then holds bf16 values exactly down to 2^-28 of the row's largest.  Softmax runs in
+// base 2 with running maxima held in float32: m over the scores for the normaliser, and
+// M over score + log2(value scale) for the weights of the value codes, which are kept as
+// fp16(2^(score + log2 scale - M + 15)): relative rounding 2^-11 down to 2^-29 of the
+// largest weight whatever the pages' scales, where a weight without its page's scale
+// could vanish next to a page of large values.
+template <int D>
+__global__ void __launch_bounds__(kStepThreads) k_attn_step(const __grid_constant__ StepArgs p) {
+    using SM = StepSmem<D>;
+    constexpr int KSTEPS = D / 16;   // 16-deep steps of the score product
+    constexpr int NT = D / 8;        // 8-column tiles of the output product
+    extern __shared__ __align__(1024) unsigned char sm[];
+    uint64_t* full = reinterpret_cast<uint64_t*>(sm + SM::kBars);
+    uint64_t* empty = full + kStepStages;
+    StepMeta* meta = reinterpret_cast<StepMeta*>(sm + SM::kMeta);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int G = p.Hq / p.Hk;
+    const int gtiles = (G + kRows - 1) / kRows;
+    const int hk = blockIdx.y / gtiles, g0 = (blockIdx.y % gtiles) * kRows;
+    const int b = blockIdx.z, split = blockIdx.x;
+
+    long long len = p.lens[b];
+    const long long cap = (long long)p.max_pages * p.page;
+    len = len < 0 ? 0 : (len > cap ? cap : len);
+    const long long first = p.window > 0 && len > p.window ? len - p.window : 0;
+    // every split takes whole stages from the stage that holds `first`
+    const long long base = first / kStepKeys * kStepKeys;
+    long long per = (len - base + p.splits - 1) / p.splits;
+    per = (per + kStepKeys - 1) / kStepKeys * kStepKeys;
+    if (per < p.min_keys) per = p.min_keys;
+    const long long lo = base + split * per;
+    const long long hi = min(len, lo + per);
+    const int nst = hi > lo ? (int)((hi - lo + kStepKeys - 1) / kStepKeys) : 0;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kStepStages; ++i) {
+            t2::mbar_init(full + i, 1);
+            t2::mbar_init(empty + i, kStepWarps);
+        }
+        t2::fence_barrier_init();
+    }
+    __syncthreads();
+    bool bad = false;
+
+    if (warp == kStepWarps) {
+        // ---- producer: page ids and scales 32 pieces ahead, one piece = min(page, 64)
+        // keys, or the 64 keys of a stage inside a longer page
+        const int piece = p.page < kStepKeys ? p.page : kStepKeys;
+        const int per_stage = kStepKeys / piece;
+        const int npiece = nst * per_stage;
+        for (int i0 = 0; i0 < npiece && !bad; i0 += 32) {
+            int id = -1;
+            float ks = 0.f, vs = 0.f;
+            const long long key = lo + (long long)(i0 + lane) * piece;
+            if (i0 + lane < npiece && key < hi) {
+                id = p.table[(long long)b * p.max_pages + key / p.page];
+                if (id < 0 || id >= p.num_pages) id = -1;
+                if (id >= 0) {
+                    ks = p.k_scale[(long long)id * p.Hk + hk];
+                    vs = p.v_scale[(long long)id * p.Hk + hk];
+                }
+            }
+            const int n = min(32, npiece - i0);
+            for (int i = 0; i < n; i += per_stage) {
+                const int st = (i0 + i) / per_stage, slot = st % kStepStages;
+                if (st >= kStepStages) {
+                    const bool ok = t2::mbar_wait(empty + slot, ((st / kStepStages) - 1) & 1);
+                    if (!__all_sync(0xffffffffu, ok)) {
+                        bad = true;
+                        break;
+                    }
+                }
+                unsigned char* kd = sm + (size_t)slot * 2 * SM::kTile;
+                // metadata of the stage's four groups of 16 keys
+                const int src = i + (lane * 16) / piece;
+                const int gid = __shfl_sync(0xffffffffu, id, src & 31);
+                const float gks = __shfl_sync(0xffffffffu, ks, src & 31);
+                const float gvs = __shfl_sync(0xffffffffu, vs, src & 31);
+                if (lane < 4) {
+                    const long long k0 = lo + (long long)st * kStepKeys + lane * 16;
+                    StepMeta m;
+                    m.ks = gks;
+                    m.lv = __log2f(gvs);
+                    m.lo = (int)max(0LL, min(16LL, first - k0));
+                    m.hi = gid < 0 ? 0 : (int)max(0LL, min(16LL, hi - k0));
+                    meta[slot * 4 + lane] = m;
+                }
+                int copies = 0;
+                for (int j = 0; j < per_stage; ++j)
+                    copies += __shfl_sync(0xffffffffu, id, (i + j) & 31) >= 0 ? 1 : 0;
+                __syncwarp();
+                if (lane == 0) t2::mbar_arrive_expect_tx(full + slot, (uint32_t)(copies * 2 * piece * D));
+                __syncwarp();
+                for (int j = 0; j < per_stage; ++j) {
+                    const int pid = __shfl_sync(0xffffffffu, id, (i + j) & 31);
+                    if (lane == 0 && pid >= 0) {
+                        const int row = (int)((lo + (long long)st * kStepKeys + j * piece) % p.page);
+                        t2::tma_load_3d(kd + (size_t)j * piece * D, &p.tk, 0, row, pid * p.Hk + hk, full + slot);
+                        t2::tma_load_3d(kd + SM::kTile + (size_t)j * piece * D, &p.tv, 0, row,
+                                        pid * p.Hk + hk, full + slot);
+                    }
+                }
+            }
+        }
+        if (bad && lane == 0) atomicOr(&g_kv_timeouts, 1u);
+        // the copies in flight land in this block's shared memory: consumers wait for
+        // each of them below before the block ends
+    }
+
+    // ---- consumers
+    const int g = lane >> 2, c = lane & 3;
+    float m[2] = {-INFINITY, -INFINITY}, M[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+    float acc[NT][4];
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[t][i] = 0.f;
+
+    if (warp < kStepWarps && nst > 0) {
+        // query fragments: rows g and g + 8; step s of the contraction takes channels
+        // c * D/4 + 4 s .. + 3 of lane c
+        uint32_t qa[KSTEPS][4];
+        float qscale[2];
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            const int head = g0 + g + 8 * r;
+            float x[D / 4];
+            float mx = 0.f;
+            const bool on = head < G;
+            const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(p.q) +
+                                     ((long long)b * p.Hq + (long long)hk * G + (on ? head : 0)) * D + c * (D / 4);
+#pragma unroll
+            for (int i = 0; i < D / 32; ++i) {
+                uint4 w = make_uint4(0u, 0u, 0u, 0u);
+                if (on) w = *reinterpret_cast<const uint4*>(q + 8 * i);
+                kv_unpack(w, x + 8 * i, __nv_bfloat16());
+            }
+#pragma unroll
+            for (int i = 0; i < D / 4; ++i) mx = fmaxf(mx, fabsf(x[i]));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+            int e = 0;
+            if (mx > 0.f && mx <= 3.4e38f) frexpf(mx, &e);
+            const int sh = 14 - e;  // in [-114, 163]: applied in two halves
+            const float s1 = ldexpf(1.f, sh / 2), s2 = ldexpf(1.f, sh - sh / 2);
+            qscale[r] = p.scale_log2 / s1 / s2;
+#pragma unroll
+            for (int s = 0; s < KSTEPS; ++s) {
+                const __half2 u = __floats2half2_rn(x[4 * s] * s1 * s2, x[4 * s + 1] * s1 * s2);
+                const __half2 v = __floats2half2_rn(x[4 * s + 2] * s1 * s2, x[4 * s + 3] * s1 * s2);
+                qa[s][r] = *reinterpret_cast<const uint32_t*>(&u);
+                qa[s][2 + r] = *reinterpret_cast<const uint32_t*>(&v);
+            }
+        }
+
+        for (int st = 0; st < nst; ++st) {
+            const int slot = st % kStepStages;
+            const bool ok = t2::mbar_wait(full + slot, (st / kStepStages) & 1);
+            if (!__all_sync(0xffffffffu, ok)) {
+                bad = true;
+                break;
+            }
+            const unsigned char* kt = sm + (size_t)slot * 2 * SM::kTile;
+            const unsigned char* vt = kt + SM::kTile;
+            const StepMeta mt = meta[slot * 4 + warp];
+            if (mt.hi > mt.lo) {  // uniform in the warp
+                float s[2][4];
+#pragma unroll
+                for (int n = 0; n < 2; ++n) {
+                    const int r = 16 * warp + 8 * n + g;
+                    s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.f;
+#pragma unroll
+                    for (int i = 0; i < D / 64; ++i) {
+                        const uint4 kw = *reinterpret_cast<const uint4*>(kt + step_off<D>(r, c * (D / 64) + i));
+                        const uint32_t w[4] = {kw.x, kw.y, kw.z, kw.w};
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            mma_f16_16816(s[n], qa[4 * i + j], h2_from_e4m3(w[j]), h2_from_e4m3_hi(w[j]));
+                    }
+                }
+                // rows g (r = 0) and g + 8 (r = 1); keys 8 n + 2 c, + 1
+                float pw[2][4];
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    const float f = qscale[r] * mt.ks;
+                    float mx = -INFINITY;
+#pragma unroll
+                    for (int n = 0; n < 2; ++n)
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            const int key = 8 * n + 2 * c + i;
+                            float& x = s[n][2 * r + i];
+                            x = (key >= mt.lo && key < mt.hi) ? x * f : -INFINITY;
+                            mx = fmaxf(mx, x);
+                        }
+                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+                    const float mn = fmaxf(m[r], mx);
+                    const float ms = mn == -INFINITY ? 0.f : mn;
+                    l[r] *= ex2(m[r] - ms);
+                    m[r] = mn;
+                    const float Mn = fmaxf(M[r], mx + mt.lv);
+                    const float Ms = Mn == -INFINITY ? 0.f : Mn;
+                    if (__any_sync(0xffffffffu, Mn != M[r])) {
+                        const float a = ex2(M[r] - Ms);
+#pragma unroll
+                        for (int t = 0; t < NT; ++t) {
+                            acc[t][2 * r] *= a;
+                            acc[t][2 * r + 1] *= a;
+                        }
+                    }
+                    M[r] = Mn;
+                    const float off = mt.lv - Ms + 15.f;
+#pragma unroll
+                    for (int n = 0; n < 2; ++n)
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            const float x = s[n][2 * r + i];
+                            l[r] += ex2(x - ms);
+                            pw[n][2 * r + i] = ex2(x + off);
+                        }
+                }
+                uint32_t pa[4];
+#pragma unroll
+                for (int n = 0; n < 2; ++n)
+#pragma unroll
+                    for (int r = 0; r < 2; ++r) {
+                        const __half2 u = __floats2half2_rn(pw[n][2 * r], pw[n][2 * r + 1]);
+                        pa[2 * n + r] = *reinterpret_cast<const uint32_t*>(&u);
+                    }
+                // value codes of keys 2c, 2c+1, 2c+8, 2c+9, columns g * D/8 .. + D/8
+                uint32_t w[4][D / 32];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int kk = 2 * c + (i & 1) + 8 * (i >> 1);
+                    const int r = 16 * warp + kk;
+                    if (D == 128) {
+                        const uint4 u = *reinterpret_cast<const uint4*>(vt + step_off<D>(r, g));
+                        w[i][0] = u.x; w[i][1] = u.y; w[i][D / 32 - 2] = u.z; w[i][D / 32 - 1] = u.w;
+                    } else {
+                        const uint2 u = *reinterpret_cast<const uint2*>(vt + step_off<D>(r, g >> 1) + 8 * (g & 1));
+                        w[i][0] = u.x; w[i][1] = u.y;
+                    }
+                    // slots behind the sequence may hold anything: no code of theirs is used
+                    if (kk < mt.lo || kk >= mt.hi) {
+#pragma unroll
+                        for (int j = 0; j < D / 32; ++j) w[i][j] = 0u;
+                    }
+                }
+#pragma unroll
+                for (int j = 0; j < D / 32; ++j) {
+                    const uint32_t a0 = __byte_perm(w[0][j], w[1][j], 0x5140), a1 = __byte_perm(w[0][j], w[1][j], 0x7362);
+                    const uint32_t b0 = __byte_perm(w[2][j], w[3][j], 0x5140), b1 = __byte_perm(w[2][j], w[3][j], 0x7362);
+                    mma_f16_16816(acc[4 * j], pa, h2_from_e4m3(a0), h2_from_e4m3(b0));
+                    mma_f16_16816(acc[4 * j + 1], pa, h2_from_e4m3_hi(a0), h2_from_e4m3_hi(b0));
+                    mma_f16_16816(acc[4 * j + 2], pa, h2_from_e4m3(a1), h2_from_e4m3(b1));
+                    mma_f16_16816(acc[4 * j + 3], pa, h2_from_e4m3_hi(a1), h2_from_e4m3_hi(b1));
+                }
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(empty + slot);
+        }
+        if (bad && lane == 0) atomicOr(&g_kv_timeouts, 2u);
+    }
+
+    // ---- the four warps' parts together: o = sum_w 2^(m_w - m) ..., through the ring's memory
+    __syncthreads();
+    float* so = reinterpret_cast<float*>(sm);               // [warp][16][D]
+    float* sml = so + kStepWarps * kRows * D;               // [warp][16][2]: m, l
+    if (warp < kStepWarps) {
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
+            l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
+            // in units of 2^m: the codes' weights carry 2^(15 - M)
+            const float u = l[r] > 0.f ? ex2(M[r] - 15.f - m[r]) : 0.f;
+            float* row = so + (warp * kRows + g + 8 * r) * D;
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+                row[(2 * c) * (D / 8) + t] = acc[t][2 * r] * u;
+                row[(2 * c + 1) * (D / 8) + t] = acc[t][2 * r + 1] * u;
+            }
+            if (c == 0) {
+                sml[(warp * kRows + g + 8 * r) * 2] = m[r];
+                sml[(warp * kRows + g + 8 * r) * 2 + 1] = l[r];
+            }
+        }
+    }
+    __syncthreads();
+    const int rows = min(kRows, G - g0);
+    for (int i = threadIdx.x; i < rows * D; i += kStepThreads) {
+        const int r = i / D, ch = i % D;
+        float mm = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < kStepWarps; ++w) mm = fmaxf(mm, sml[(w * kRows + r) * 2]);
+        const float ms = mm == -INFINITY ? 0.f : mm;
+        float sum = 0.f, o = 0.f;
+#pragma unroll
+        for (int w = 0; w < kStepWarps; ++w) {
+            const float f = ex2(sml[(w * kRows + r) * 2] - ms);
+            sum += f * sml[(w * kRows + r) * 2 + 1];
+            o += f * so[(w * kRows + r) * D + ch];
+        }
+        o = sum > 0.f || sum != sum ? o / sum : 0.f;
+        const long long head = (long long)b * p.Hq + (long long)hk * G + g0 + r;
+        if (p.splits == 1) {
+            static_cast<__nv_bfloat16*>(p.o)[head * D + ch] = __float2bfloat16_rn(o);
+        } else {
+            p.part[(head * p.splits + split) * D + ch] = o;
+            if (ch == 0) p.part_lse[head * p.splits + split] = sum > 0.f || sum != sum ? ms + __log2f(sum) : -INFINITY;
+        }
+    }
+}
+
+// Splits of a sequence and head together: weights 2^(lse_i - max).
+template <int D>
+__global__ void __launch_bounds__(D) k_attn_step_join(const float* part, const float* lse, __nv_bfloat16* o,
+                                                      int splits) {
+    const long long head = blockIdx.x;
+    const int ch = threadIdx.x;
+    float mx = -INFINITY;
+    for (int i = 0; i < splits; ++i) mx = fmaxf(mx, lse[head * splits + i]);
+    const float ms = mx == -INFINITY ? 0.f : mx;
+    float sum = 0.f, a = 0.f;
+    for (int i = 0; i < splits; ++i) {
+        const float e = lse[head * splits + i];
+        if (e == -INFINITY) continue;
+        const float f = ex2(e - ms);
+        sum += f;
+        a += f * part[(head * splits + i) * D + ch];
+    }
+    o[head * D + ch] = __float2bfloat16_rn(sum > 0.f || sum != sum ? a / sum : 0.f);
+}
+
+}  // namespace
+
+cudaError_t launch_kv_append(const AppendArgs& a, int B, int d, bool bf16, cudaStream_t st) {
+    const dim3 grid((a.T + a.page - 2) / a.page + 1, a.Hk, 2 * B);
+    if (bf16) {
+        if (d == 128) MUIR_TIMED("k_kv_append", st, k_kv_append<__nv_bfloat16, 128><<<grid, kAppThreads, 0, st>>>(a));
+        else MUIR_TIMED("k_kv_append", st, k_kv_append<__nv_bfloat16, 64><<<grid, kAppThreads, 0, st>>>(a));
+    } else {
+        if (d == 128) MUIR_TIMED("k_kv_append", st, k_kv_append<float, 128><<<grid, kAppThreads, 0, st>>>(a));
+        else MUIR_TIMED("k_kv_append", st, k_kv_append<float, 64><<<grid, kAppThreads, 0, st>>>(a));
+    }
+    return cudaGetLastError();
+}
+
+int attn_step_splits(int B, int Hq, int Hk, int page, int max_pages) {
+    const long long units = (long long)B * Hk * ((Hq / Hk + kRows - 1) / kRows);
+    const long long cap = (long long)page * max_pages;
+    // enough blocks for the resident ones of 148 SMs, and none longer than 2048 keys, so
+    // that one long sequence of a ragged batch does not run on after the others
+    long long s = (2 * 148 + units - 1) / units;
+    const long long by_len = (cap + 2047) / 2048;
+    if (s < by_len) s = by_len;
+    const long long most = (cap + 255) / 256;
+    if (s > most) s = most;
+    if (s > 128) s = 128;
+    return s < 1 ? 1 : (int)s;
+}
+
+size_t attn_step_ws_bytes(int B, int Hq, int Hk, int d, int page, int max_pages) {
+    const size_t s = attn_step_splits(B, Hq, Hk, page, max_pages);
+    return s == 1 ? 0 : (size_t)B * Hq * s * (d + 1) * 4;
+}
+
+cudaError_t launch_attn_step(StepArgs a, int B, int d, void* ws, cudaStream_t st) {
+    a.splits = attn_step_splits(B, a.Hq, a.Hk, a.page, a.max_pages);
+    a.min_keys = 256;
+    a.part = static_cast<float*>(ws);
+    a.part_lse = a.part + (size_t)B * a.Hq * a.splits * d;
+    const int piece = a.page < kStepKeys ? a.page : kStepKeys;
+    cudaError_t err = make_tmap_u8(&a.tk, a.k_pages, d, a.page, (uint64_t)a.num_pages * a.Hk, piece);
+    if (err != cudaSuccess) return err;
+    err = make_tmap_u8(&a.tv, a.v_pages, d, a.page, (uint64_t)a.num_pages * a.Hk, piece);
+    if (err != cudaSuccess) return err;
+    const int gt = (a.Hq / a.Hk + kRows - 1) / kRows;
+    const dim3 grid(a.splits, a.Hk * gt, B);
+    if (d == 128) {
+        err = cudaFuncSetAttribute(k_attn_step<128>, cudaFuncAttributeMaxDynamicSharedMemorySize, StepSmem<128>::kBytes);
+        if (err != cudaSuccess) return err;
+        MUIR_TIMED("k_attn_step", st, k_attn_step<128><<<grid, kStepThreads, StepSmem<128>::kBytes, st>>>(a));
+    } else {
+        err = cudaFuncSetAttribute(k_attn_step<64>, cudaFuncAttributeMaxDynamicSharedMemorySize, StepSmem<64>::kBytes);
+        if (err != cudaSuccess) return err;
+        MUIR_TIMED("k_attn_step", st, k_attn_step<64><<<grid, kStepThreads, StepSmem<64>::kBytes, st>>>(a));
+    }
+    err = cudaGetLastError();
+    if (err != cudaSuccess || a.splits == 1) return err;
+    if (d == 128)
+        MUIR_TIMED("k_attn_step_join", st, k_attn_step_join<128><<<B * a.Hq, 128, 0, st>>>(
+            a.part, a.part_lse, static_cast<__nv_bfloat16*>(a.o), a.splits));
+    else
+        MUIR_TIMED("k_attn_step_join", st, k_attn_step_join<64><<<B * a.Hq, 64, 0, st>>>(
+            a.part, a.part_lse, static_cast<__nv_bfloat16*>(a.o), a.splits));
+    return cudaGetLastError();
+}
+
+unsigned int timeouts_kv() {
+    unsigned int n = 0;
+    cudaMemcpyFromSymbol(&n, g_kv_timeouts, sizeof(n));
+    const unsigned int z = 0;
+    cudaMemcpyToSymbol(g_kv_timeouts, &z, sizeof(z));
+    return n;
+}
+
+}  // namespace muir

@@ -1,0 +1,21 @@
+// tmap.h -- tensor maps of the attention layer's kernels (host side).
+#pragma once
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+namespace muir {
+
+// Token-major 16-bit tensor [tokens][heads][d] whose tokens lie `ld` elements apart:
+// boxes of 64 channels x 1 head x `box_tokens` tokens, 128-byte swizzle.  Coordinates
+// (channel, head, token); what lies past the last token reads as zero.
+cudaError_t make_tmap_tokens(CUtensorMap* m, const void* base, int d, int heads, long long ld,
+                             uint64_t tokens, int box_tokens);
+
+// Cache pages of 8-bit codes [blocks][page][d]: boxes of one block's `box_rows` rows of d
+// codes, swizzled over the row's d bytes (64 or 128).  Coordinates (channel, row, block).
+cudaError_t make_tmap_u8(CUtensorMap* m, const void* base, int d, int page, uint64_t blocks,
+                         int box_rows);
+
+}  // namespace muir

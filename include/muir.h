@@ -369,6 +369,95 @@ muir_status muir_qk_prologue(long long rows, int d, muir_dtype dtype, const void
 muir_status muir_qk_prologue_bwd(long long rows, int d, muir_dtype dtype, const void* x,
                                  const void* dy, void* dx, void* stream);
 
+/*
+ * Rotary positions, for the softmax-attention layers of a stack that mixes them
+ * with gated-delta-rule layers (the recurrence takes its order from the state).
+ * Per token at position p, on pairs (a, b) of the first `rot` channels:
+ *
+ *     (a, b) -> mscale * (a cos t - b sin t, b cos t + a sin t),  t = p * inv_freq[i]
+ *
+ *   interleaved : 1 = pairs (2i, 2i+1); 0 = pairs (i, i + rot/2)
+ *   inverse     : 1 = the transpose (-t): the gradient of the call with 0
+ *   q, k        : [B][T][Hq][d], [B][T][Hk][d] in dtype; *_ld elements between
+ *                 tokens (0 = heads * d), so that q and k may be parts of one
+ *                 projection's rows; k may be NULL with Hk = 0
+ *   q_out, k_out: the same shapes, with leading dimensions of their own; may
+ *                 equal the inputs (in place, equal leading dimensions then) and
+ *                 must not otherwise overlap them
+ *   positions   : device int32 [B][T], or NULL = the token's index 0 .. T-1
+ *   inv_freq    : device float64 [rot/2], radians per position.  Angles are formed
+ *                 and reduced in float64: exact to float32 rounding at any position
+ *   rot         : a multiple of 16, 16 <= rot <= d; channels past it pass through
+ * d is 64 or 128, leading dimensions are multiples of 16 bytes (8 or 4 elements).
+ * B * T = 0 enqueues nothing.  Float32 arithmetic, rounded once to dtype.
+ */
+muir_status muir_rotary(int B, int T, int Hq, int Hk, int d, int rot, muir_dtype dtype,
+                        const void* q, long long q_ld, const void* k, long long k_ld,
+                        const int* positions, const double* inv_freq, float mscale,
+                        int interleaved, int inverse, void* q_out, long long q_out_ld,
+                        void* k_out, long long k_out_ld, void* stream);
+
+/*
+ * Paged key/value cache of 8-bit values for an attention layer's decoding.
+ * A page holds `page` tokens (16, 32, 64 or 128) of all Hk key heads:
+ *
+ *   k_pages, v_pages : [num_pages][Hk][page][d] e4m3 codes
+ *   k_scale, v_scale : [num_pages][Hk] float32; value = code * scale
+ *   table            : device int32 [B][max_pages]; token t of sequence b lies in
+ *                      page table[b][t / page], row t % page.  Entries outside
+ *                      0 .. num_pages-1 name no page: nothing is written there,
+ *                      and its tokens are not attended to
+ */
+typedef struct {
+    int Hk, d, page, num_pages;
+    int max_pages;              /* entries of a sequence's row of the table */
+    void *k_pages, *v_pages;
+    float *k_scale, *v_scale;
+    const int* table;
+} muir_kv_cache;
+
+/*
+ * Writes new tokens into the cache, rounded to e4m3 under one power-of-two scale
+ * for each (page, head).  Sequence b's tokens 0 .. count[b]-1 of k and v go to
+ * positions start[b] .. start[b]+count[b]-1.
+ *
+ *   k, v  : [B][T][Hk][d] in dtype, *_ld elements between tokens (0 = Hk * d)
+ *   start : device int32 [B], tokens the sequence already has (the sequence is
+ *           left alone where it is negative)
+ *   count : device int32 [B], clamped to 0 .. T; NULL = T
+ * A page's scale is the smallest power of two (at least 2^-100) under which the
+ * largest finite magnitude among its tokens fits in 448, and never shrinks while
+ * the page fills: where it grows, the codes already held are encoded again (exact,
+ * but for codes that become subnormal).  The scale that a page held before its
+ * first row is written is ignored.  Infinities are stored as +-448, NaN as NaN.
+ * Tokens past max_pages * page are dropped.  Rows behind the new tokens keep what
+ * they hold.  No two sequences of one call may write to the same page.
+ */
+muir_status muir_kv_append(int B, int T, muir_dtype dtype, const void* k, long long k_ld,
+                           const void* v, long long v_ld, const muir_kv_cache* cache,
+                           const int* start, const int* count, void* stream);
+
+/*
+ * One query token of every sequence attends over its cached tokens (the
+ * attention layer's muir_recurrent_step):
+ *
+ *     o = sum_j softmax_j(scale q . k_j) v_j,   max(0, lens[b] - window) <= j < lens[b]
+ *
+ *   q, o   : [B][Hq][d] bfloat16; query heads h Hq/Hk .. (h+1) Hq/Hk - 1 share key head h
+ *   lens   : device int32 [B], clamped to 0 .. max_pages * page; o = 0 where no
+ *            token is visible
+ *   window : 0 = every token, else the last `window` ones
+ * Products in fp16 with float32 sums (the codes are exact in fp16), softmax in
+ * float32.  Bound by HBM: the visible codes are read once for up to 16 query heads
+ * of a key head.  Work is split over the length; the parts are joined in a fixed
+ * order, so results repeat bit for bit.  The workspace (query below; 0 bytes when
+ * nothing is split) belongs to the call until it has finished.
+ */
+size_t muir_attn_step_workspace(int B, int Hq, const muir_kv_cache* cache);
+muir_status muir_attn_step(int B, int Hq, const muir_kv_cache* cache, const void* q,
+                           const int* lens, float scale, int window, void* o, void* ws,
+                           size_t ws_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif
