@@ -25,7 +25,8 @@ import torch
 __all__ = [
     "MuirError", "lib", "chunk_fwd", "chunk_bwd", "chunk_fwd_varlen", "chunk_bwd_varlen",
     "recurrent_step", "qk_prologue", "chunk_fwd_fused", "chunk_bwd_fused", "MuirFusion",
-    "qk_prologue_bwd", "rotary", "rotary_frequencies", "kv_cache", "kv_append", "attn_step",
+    "qk_prologue_bwd", "rotary", "rotary_frequencies", "attn_fwd", "attn_bwd",
+    "attn_fwd_varlen", "attn_bwd_varlen", "MuirAttentionFunction", "kv_cache", "kv_append", "attn_step",
     "fwd_workspace_bytes", "bwd_workspace_bytes", "MuirChunkFunction",
     "LIB_PATH",
 ]
@@ -63,6 +64,14 @@ class MuirFusion(ctypes.Structure):
 class MuirFusionGrads(ctypes.Structure):
     _fields_ = [("dlatent", ctypes.c_void_p), ("dU", ctypes.c_void_p * 5),
                 ("dbias", ctypes.c_void_p * 5)]
+
+
+class MuirAttnShape(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int), ("Tq", ctypes.c_int), ("Tk", ctypes.c_int),
+                ("Hq", ctypes.c_int), ("Hk", ctypes.c_int), ("d", ctypes.c_int),
+                ("causal", ctypes.c_int), ("window", ctypes.c_int), ("scale", ctypes.c_float),
+                ("q_ld", ctypes.c_longlong), ("k_ld", ctypes.c_longlong),
+                ("v_ld", ctypes.c_longlong)]
 
 
 class MuirKvCache(ctypes.Structure):
@@ -130,6 +139,17 @@ def lib():
         LL, F, CP = ctypes.c_longlong, ctypes.c_float, ctypes.POINTER(MuirKvCache)
         L.muir_rotary.argtypes = [I] * 7 + [P, LL, P, LL, P, P, F, I, I, P, LL, P, LL, P]
         L.muir_rotary.restype = I
+        AP, LLA = ctypes.POINTER(MuirAttnShape), ctypes.POINTER(ctypes.c_longlong)
+        L.muir_attn_fwd.argtypes = [AP] + [P] * 6
+        L.muir_attn_fwd.restype = I
+        L.muir_attn_bwd_workspace.argtypes = [AP]
+        L.muir_attn_bwd_workspace.restype = S
+        L.muir_attn_bwd.argtypes = [AP] + [P] * 10 + [S, P]
+        L.muir_attn_bwd.restype = I
+        L.muir_attn_fwd_varlen.argtypes = [AP, I, LLA, LLA] + [P] * 6
+        L.muir_attn_fwd_varlen.restype = I
+        L.muir_attn_bwd_varlen.argtypes = [AP, I, LLA, LLA] + [P] * 10 + [S, P]
+        L.muir_attn_bwd_varlen.restype = I
         L.muir_kv_append.argtypes = [I, I, I, P, LL, P, LL, CP, P, P, P]
         L.muir_kv_append.restype = I
         L.muir_attn_step_workspace.argtypes = [I, I, CP]
@@ -598,6 +618,88 @@ def rotary(q, k=None, positions=None, inv_freq=None, interleaved=False, mscale=1
     return q_out if k is None else (q_out, k_out)
 
 
+def _attn_shape(q, k, v, causal, window, scale):
+    """(MuirAttnShape, addresses of q, k, v)."""
+    B, Tq, Hq, d = q.shape
+    Bk, Tk, Hk, dk = k.shape
+    dev = q.device
+    if Bk != B or dk != d or v.shape != k.shape:
+        raise ValueError("q, k and v must agree in batch and channels, k and v in shape")
+    if q.dtype != torch.bfloat16 or k.dtype != torch.bfloat16 or v.dtype != torch.bfloat16:
+        raise TypeError("attention takes bfloat16 tensors")
+    qp, ql = _rows(q, "q")
+    kp, kl = _rows(k, "k", dev)
+    vp, vl = _rows(v, "v", dev)
+    return MuirAttnShape(B, Tq, Tk, Hq, Hk, d, 1 if causal else 0, window,
+                         d ** -0.5 if scale is None else scale, ql, kl, vl), qp, kp, vp
+
+
+def attn_fwd(q, k, v, causal=True, window=0, scale=None):
+    """Softmax attention (``muir_attn_fwd``) of bfloat16 ``q [B, Tq, Hq, d]`` over
+    ``k, v [B, Tk, Hk, d]`` (parts of a packed projection are taken as they lie).  Query i
+    stands at key position ``i + Tk - Tq``; ``causal`` hides later keys, ``window`` all but
+    the last ``window``.  ``scale`` defaults to ``d ** -0.5``.  Returns ``(o, lse)`` with
+    ``o [B, Tq, Hq, d]`` and float32 ``lse [B, Hq, Tq]``."""
+    s, qp, kp, vp = _attn_shape(q, k, v, causal, window, scale)
+    o = torch.empty(s.B, s.Tq, s.Hq, s.d, dtype=torch.bfloat16, device=q.device)
+    lse = torch.empty(s.B, s.Hq, s.Tq, dtype=torch.float32, device=q.device)
+    _dev_call("muir_attn_fwd", q, ctypes.byref(s), qp, kp, vp, o.data_ptr(), lse.data_ptr())
+    return o, lse
+
+
+def _attn_bwd(name, extra, q, k, v, o, lse, dO, causal, window, scale, ws):
+    s, qp, kp, vp = _attn_shape(q, k, v, causal, window, scale)
+    dev = q.device
+    shape = (s.B, s.Tq, s.Hq, s.d)
+    op = _same(o, "o", shape, torch.bfloat16, dev)
+    gp = _same(dO, "dO", shape, torch.bfloat16, dev)
+    lp = _same(lse, "lse", (s.B, s.Hq, s.Tq), torch.float32, dev)
+    grads = {"dq": torch.empty(shape, dtype=torch.bfloat16, device=dev)}
+    for n in ("dk", "dv"):
+        grads[n] = torch.empty(s.B, s.Tk, s.Hk, s.d, dtype=torch.bfloat16, device=dev)
+    wsb = _workspace(lib().muir_attn_bwd_workspace(ctypes.byref(s)), dev, ws)
+    _dev_call(name, q, ctypes.byref(s), *extra, qp, kp, vp, op, lp, gp, grads["dq"].data_ptr(),
+              grads["dk"].data_ptr(), grads["dv"].data_ptr(),
+              None if wsb is None else wsb.data_ptr(), 0 if wsb is None else wsb.numel())
+    return grads
+
+
+def attn_bwd(q, k, v, o, lse, dO, causal=True, window=0, scale=None, ws=None):
+    """Gradients of ``sum(o * dO)`` (``muir_attn_bwd``) from :func:`attn_fwd`'s ``o`` and
+    ``lse``; the probabilities are recomputed.  Returns a dict with ``dq, dk, dv``."""
+    return _attn_bwd("muir_attn_bwd", (), q, k, v, o, lse, dO, causal, window, scale, ws)
+
+
+def _cu_pair(cu_seqlens, cu_seqlens_k):
+    n, cu = _cu(cu_seqlens)
+    if cu_seqlens_k is None:
+        return n, cu, None
+    nk, ck = _cu(cu_seqlens_k)
+    if nk != n:
+        raise ValueError("cu_seqlens_k must have as many offsets as cu_seqlens")
+    return n, cu, ck
+
+
+def attn_fwd_varlen(q, k, v, cu_seqlens, cu_seqlens_k=None, causal=True, window=0, scale=None):
+    """:func:`attn_fwd` over packed sequences: ``q [1, T, Hq, d]``, ``k, v [1, Tk, Hk, d]`` with
+    sequence i at rows ``cu_seqlens[i]:cu_seqlens[i+1]`` (a host list or CPU tensor;
+    ``cu_seqlens_k`` for the keys where they differ).  ``lse`` is ``[1, Hq, T]``."""
+    n, cu, ck = _cu_pair(cu_seqlens, cu_seqlens_k)
+    s, qp, kp, vp = _attn_shape(q, k, v, causal, window, scale)
+    o = torch.empty(s.B, s.Tq, s.Hq, s.d, dtype=torch.bfloat16, device=q.device)
+    lse = torch.empty(s.B, s.Hq, s.Tq, dtype=torch.float32, device=q.device)
+    _dev_call("muir_attn_fwd_varlen", q, ctypes.byref(s), n, cu, ck, qp, kp, vp, o.data_ptr(),
+              lse.data_ptr())
+    return o, lse
+
+
+def attn_bwd_varlen(q, k, v, o, lse, dO, cu_seqlens, cu_seqlens_k=None, causal=True, window=0,
+                    scale=None, ws=None):
+    """Gradients through :func:`attn_fwd_varlen`; returns the dict of :func:`attn_bwd`."""
+    return _attn_bwd("muir_attn_bwd_varlen", _cu_pair(cu_seqlens, cu_seqlens_k), q, k, v, o, lse,
+                     dO, causal, window, scale, ws)
+
+
 def kv_cache(num_pages, Hk, page, d, device="cuda"):
     """Fresh cache tensors ``(k_pages, v_pages, k_scale, v_scale)``: float8_e4m3fn codes
     ``[num_pages, Hk, page, d]`` and float32 scales ``[num_pages, Hk]``."""
@@ -683,3 +785,25 @@ class MuirChunkFunction(torch.autograd.Function):
                        chunk=ctx.chunk, S_chunks=Sc, M_chunks=Mc, aux=aux)
         return (gr["dq"], gr["dk"], gr["dv"], gr["dg"], gr["de"], gr["dw"], gr["dgamma"],
                 gr["dS0"] if S0 is not None else None, None)
+
+
+class MuirAttentionFunction(torch.autograd.Function):
+    """Autograd wrapper of :func:`attn_fwd` / :func:`attn_bwd`, or of the varlen forms with
+    ``cu_seqlens``; returns ``o``."""
+
+    @staticmethod
+    def forward(ctx, q, k, v, causal=True, window=0, scale=None, cu_seqlens=None, cu_seqlens_k=None):
+        ctx.args = dict(causal=causal, window=window, scale=scale)
+        ctx.cu = None if cu_seqlens is None else dict(cu_seqlens=cu_seqlens, cu_seqlens_k=cu_seqlens_k)
+        o, lse = (attn_fwd(q, k, v, **ctx.args) if ctx.cu is None
+                  else attn_fwd_varlen(q, k, v, **ctx.cu, **ctx.args))
+        ctx.save_for_backward(q, k, v, o, lse)
+        return o
+
+    @staticmethod
+    def backward(ctx, dO):
+        saved = ctx.saved_tensors
+        dO = dO.contiguous().to(torch.bfloat16)
+        g = (attn_bwd(*saved, dO, **ctx.args) if ctx.cu is None
+             else attn_bwd_varlen(*saved, dO, **ctx.cu, **ctx.args))
+        return g["dq"], g["dk"], g["dv"], None, None, None, None, None

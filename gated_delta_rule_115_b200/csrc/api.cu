@@ -4,6 +4,7 @@
 #include <stdint.h>
 
 #include "../../include/muir.h"
+#include "attn.h"
 #include "checks.h"
 #include "chunk_units.h"
 #include "bwd2.h"
@@ -91,7 +92,8 @@ muir_status muir_device_wait_status(void) {
                            muir::timeouts_f32_d128() + muir::timeouts_f32_d64() +
                            muir::v2::timeouts_v2() + muir::v2::timeouts_bwd2() +
                            muir::timeouts_selftest() + muir::v2::timeouts_gates() +
-                           muir::timeouts_kv();
+                           muir::timeouts_kv() + muir::attn::timeouts_fwd() +
+                           muir::attn::timeouts_bwd();
     return n ? MUIR_ERR_DEVICE_TIMEOUT : MUIR_OK;
 }
 

@@ -2,6 +2,7 @@
 // argument checks, workspace sizing and dispatch to the CUDA kernels.
 #include <math.h>
 
+#include "attn.h"
 #include "checks.h"
 #include "kernels.h"
 
@@ -17,6 +18,90 @@ constexpr float kLog2e = 1.4426950408889634f;
 // and whole 16-byte vectors.
 bool ok_ld(long long ld, long long width, int esize) {
     return ld == 0 || (ld >= width && ld % (16 / esize) == 0 && ld <= (1LL << 40) / 16);
+}
+
+muir_status check_attn(const muir_attn_shape* s) {
+    if (!s) return MUIR_ERR_INVALID_ARG;
+    if (s->B < 0 || s->Tq < 0 || s->Tk < 0 || s->Hq <= 0 || s->Hk <= 0 || s->d <= 0 || s->window < 0)
+        return MUIR_ERR_INVALID_ARG;
+    if (!(s->scale > 0.f) || !isfinite(s->scale) || s->Hq % s->Hk) return MUIR_ERR_INVALID_ARG;
+    if (s->d != 64 && s->d != 128) return MUIR_ERR_UNSUPPORTED;
+    const long long wq = (long long)s->Hq * s->d, wk = (long long)s->Hk * s->d;
+    if (!ok_ld(s->q_ld, wq, 2) || !ok_ld(s->k_ld, wk, 2) || !ok_ld(s->v_ld, wk, 2)) return MUIR_ERR_INVALID_ARG;
+    // rows are int32 (with room for a tile past the end), blocks of 128 rows and heads a grid
+    if ((long long)s->B * s->Tq > 0x7fff0000LL || (long long)s->B * s->Tk > 0x7fff0000LL || s->Hq > 65536)
+        return MUIR_ERR_UNSUPPORTED;
+    const long long tq = (s->Tq + 127LL) / 128, tk = (s->Tk + 127LL) / 128;
+    if ((s->B * tq + 65536) * s->Hq > 0x7fffffffLL || (s->B * tk + 65536) * s->Hk > 0x7fffffffLL)
+        return MUIR_ERR_UNSUPPORTED;
+    return MUIR_OK;
+}
+
+muir_status check_offsets(const long long* cu, int n, int total) {
+    if (cu[0] != 0 || cu[n] != total) return MUIR_ERR_INVALID_ARG;
+    for (int i = 0; i < n; ++i)
+        if (cu[i + 1] < cu[i]) return MUIR_ERR_INVALID_ARG;
+    return MUIR_OK;
+}
+
+muir_status check_attn_varlen(const muir_attn_shape* s, int n, const long long* cu_q, const long long* cu_k) {
+    muir_status st = check_attn(s);
+    if (st != MUIR_OK) return st;
+    if (s->B != 1 || n <= 0 || !cu_q) return MUIR_ERR_INVALID_ARG;
+    if ((st = check_offsets(cu_q, n, s->Tq)) != MUIR_OK) return st;
+    return check_offsets(cu_k ? cu_k : cu_q, n, s->Tk);
+}
+
+muir::attn::Problem attn_problem(const muir_attn_shape* s, const void* q, const void* k, const void* v,
+                                 int n, const long long* cu_q, const long long* cu_k) {
+    muir::attn::Problem p;
+    p.Hq = s->Hq; p.Hk = s->Hk; p.d = s->d;
+    p.causal = s->causal != 0; p.window = s->window; p.scale = s->scale;
+    p.q_ld = s->q_ld ? s->q_ld : (long long)s->Hq * s->d;
+    p.k_ld = s->k_ld ? s->k_ld : (long long)s->Hk * s->d;
+    p.v_ld = s->v_ld ? s->v_ld : (long long)s->Hk * s->d;
+    p.q_rows = (long long)s->B * s->Tq;
+    p.k_rows = (long long)s->B * s->Tk;
+    // [B][Hq][Tq], or [Hq][Tq] over packed sequences
+    p.lse_seq = cu_q ? 1 : s->Hq;
+    p.lse_head = s->Tq;
+    p.q = q; p.k = k; p.v = v;
+    p.n = cu_q ? n : s->B;
+    p.Tq = s->Tq; p.Tk = s->Tk;
+    p.cu_q = cu_q;
+    p.cu_k = cu_k ? cu_k : cu_q;
+    return p;
+}
+
+// Pointers of tensors without elements may be null.
+bool ok_some(const void* p, bool any) { return any ? ok_ptr(p) : true; }
+
+muir_status attn_fwd(const muir_attn_shape* s, int n, const long long* cu_q, const long long* cu_k, const void* q,
+                     const void* k, const void* v, void* o, float* lse, void* stream) {
+    const bool any_q = s->B > 0 && s->Tq > 0, any_k = s->B > 0 && s->Tk > 0;
+    if (!ok_some(q, any_q) || !ok_some(o, any_q) || !ok_some(k, any_k) || !ok_some(v, any_k) ||
+        (any_q && (!lse || !aligned_to(lse, 4))))
+        return MUIR_ERR_INVALID_ARG;
+    const muir_status st = check_device();
+    if (st != MUIR_OK) return st;
+    return from_cuda(muir::attn::run_fwd(attn_problem(s, q, k, v, n, cu_q, cu_k), o, lse,
+                                         static_cast<cudaStream_t>(stream)));
+}
+
+muir_status attn_bwd(const muir_attn_shape* s, int n, const long long* cu_q, const long long* cu_k, const void* q,
+                     const void* k, const void* v, const void* o, const float* lse, const void* dO, void* dq,
+                     void* dk, void* dv, void* ws, size_t ws_bytes, void* stream) {
+    const bool any_q = s->B > 0 && s->Tq > 0, any_k = s->B > 0 && s->Tk > 0;
+    if (!ok_some(q, any_q) || !ok_some(o, any_q) || !ok_some(dO, any_q) || !ok_some(dq, any_q) ||
+        !ok_some(k, any_k) || !ok_some(v, any_k) || !ok_some(dk, any_k) || !ok_some(dv, any_k) ||
+        (any_q && (!lse || !aligned_to(lse, 4))))
+        return MUIR_ERR_INVALID_ARG;
+    const muir::attn::Problem p = attn_problem(s, q, k, v, n, cu_q, cu_k);
+    const size_t need = muir::attn::bwd_ws_bytes(p);
+    if (ws_bytes < need || (need > 0 && !ok_ptr(ws))) return MUIR_ERR_WORKSPACE;
+    const muir_status st = check_device();
+    if (st != MUIR_OK) return st;
+    return from_cuda(muir::attn::run_bwd(p, o, lse, dO, dq, dk, dv, ws, static_cast<cudaStream_t>(stream)));
 }
 
 muir_status check_cache(const muir_kv_cache* c) {
@@ -82,6 +167,40 @@ muir_status muir_rotary(int B, int T, int Hq, int Hk, int d, int rot, muir_dtype
     const muir_status st = check_device();
     if (st != MUIR_OK) return st;
     return from_cuda(muir::launch_rotary(a, dtype == MUIR_BF16, interleaved != 0, static_cast<cudaStream_t>(stream)));
+}
+
+muir_status muir_attn_fwd(const muir_attn_shape* s, const void* q, const void* k, const void* v, void* o,
+                          float* lse, void* stream) {
+    const muir_status st = check_attn(s);
+    return st != MUIR_OK ? st : attn_fwd(s, 0, nullptr, nullptr, q, k, v, o, lse, stream);
+}
+
+size_t muir_attn_bwd_workspace(const muir_attn_shape* s) {
+    if (check_attn(s) != MUIR_OK) return 0;
+    return muir::attn::bwd_ws_bytes(attn_problem(s, nullptr, nullptr, nullptr, 0, nullptr, nullptr));
+}
+
+muir_status muir_attn_bwd(const muir_attn_shape* s, const void* q, const void* k, const void* v, const void* o,
+                          const float* lse, const void* dO, void* dq, void* dk, void* dv, void* ws,
+                          size_t ws_bytes, void* stream) {
+    const muir_status st = check_attn(s);
+    return st != MUIR_OK ? st
+                         : attn_bwd(s, 0, nullptr, nullptr, q, k, v, o, lse, dO, dq, dk, dv, ws, ws_bytes, stream);
+}
+
+muir_status muir_attn_fwd_varlen(const muir_attn_shape* s, int n, const long long* cu_q, const long long* cu_k,
+                                 const void* q, const void* k, const void* v, void* o, float* lse, void* stream) {
+    const muir_status st = check_attn_varlen(s, n, cu_q, cu_k);
+    return st != MUIR_OK ? st : attn_fwd(s, n, cu_q, cu_k, q, k, v, o, lse, stream);
+}
+
+muir_status muir_attn_bwd_varlen(const muir_attn_shape* s, int n, const long long* cu_q, const long long* cu_k,
+                                 const void* q, const void* k, const void* v, const void* o, const float* lse,
+                                 const void* dO, void* dq, void* dk, void* dv, void* ws, size_t ws_bytes,
+                                 void* stream) {
+    const muir_status st = check_attn_varlen(s, n, cu_q, cu_k);
+    return st != MUIR_OK ? st
+                         : attn_bwd(s, n, cu_q, cu_k, q, k, v, o, lse, dO, dq, dk, dv, ws, ws_bytes, stream);
 }
 
 muir_status muir_kv_append(int B, int T, muir_dtype dtype, const void* k, long long k_ld,

@@ -1,0 +1,669 @@
+// attn_bwd.cu -- softmax attention, backward, on tcgen05.
+//
+//     p_ij  = exp(s_ij - lse_i)                       (recomputed; s_ij = scale q_i . k_j)
+//     dv_j  = sum_i p_ij dO_i
+//     ds_ij = p_ij (dO_i . v_j - D_i),                D_i = dO_i . o_i
+//     dq_i  = scale sum_j ds_ij k_j,     dk_j = scale sum_i ds_ij q_i
+//
+// Three kernels: D; then dk and dv, a block owning 128 keys of one key head and walking the
+// queries of its group's heads; then dq, a block owning 128 queries and walking the keys.
+// Each sum is therefore formed by one block, in tensor memory, in a fixed order: no atomics,
+// no float32 gradient buffers, and shared key heads need no second pass.  The price is that
+// the scores and dO . v are formed twice (7 products a pair of tiles, where 5 would do if dq
+// were scattered).
+//
+// In both, tensor memory holds the scores of a step (S, 128 columns), dO . v (P, 128) and the
+// sums.  Eight warps take a row and 64 of the 128 columns a thread, turn the scores into p and
+// the pair into ds, and write them, rounded to bf16 (half a step, 2^-8), over the columns of S
+// that they have read, where they are the A operand of the products that follow.
+//
+//   warps 0-3, 4-7 : p and ds of columns 0-63, 64-127     warp 8 : issues every product
+//   warp 9         : loads (TMA)
+//
+// Bound by the tensor cores (14 d flops a visible pair here) with the exponentials close
+// behind (2 a pair, 16 a clock and SM).
+#include "attn_dev.cuh"
+#include "profile.h"
+#include "tmap.h"
+
+namespace muir {
+namespace attn {
+
+__device__ unsigned int g_bwd_timeouts;
+
+namespace {
+
+constexpr int kThreads = 320;
+constexpr float kLog2e = 1.4426950408889634f;
+
+struct BwdParams {
+    CUtensorMap tq, tk, tv, tdo;
+    const float *lse, *delta;
+    __nv_bfloat16 *dq, *dk, *dv;
+    long long lse_seq, lse_head;
+    float scale, scale_log2;
+    int Hq, Hk, causal, window, n;
+    Seq seq[kMaxSeqs];
+};
+
+// ------------------------------------------------------------------ D = dO . o
+
+// A row of D channels is D / 8 lanes; one float32 a (token, head).
+template <int D>
+__global__ void __launch_bounds__(256) k_attn_delta(const __nv_bfloat16* __restrict__ o,
+                                                    const __nv_bfloat16* __restrict__ dO, float* __restrict__ delta,
+                                                    long long rows, int Hq, int T, long long lse_seq,
+                                                    long long lse_head) {
+    constexpr int G = D / 8;
+    const int lane = threadIdx.x & 31, sub = lane / G;
+    const long long r = ((long long)blockIdx.x * 8 + (threadIdx.x >> 5)) * (32 / G) + sub;
+    float s = 0.f;
+    if (r < rows) {
+        const uint4 a = *reinterpret_cast<const uint4*>(o + r * D + (lane % G) * 8);
+        const uint4 b = *reinterpret_cast<const uint4*>(dO + r * D + (lane % G) * 8);
+        const uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            float x0, x1, y0, y1;
+            unpack16<true>(x[i], x0, x1);
+            unpack16<true>(y[i], y0, y1);
+            s += x0 * y0 + x1 * y1;
+        }
+    }
+#pragma unroll
+    for (int off = G / 2; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
+    if (r < rows && lane % G == 0) {
+        // token-major rows -> the layout of lse
+        const long long tok = r / Hq;
+        const int h = (int)(r - tok * Hq);
+        const long long b = lse_seq == 1 ? 0 : tok / T;
+        delta[b * T * lse_seq + h * lse_head + (tok - b * T)] = s;
+    }
+}
+
+// ------------------------------------------------------------------ dk, dv
+
+template <int D>
+struct BwdSmem {
+    static constexpr int kTileBytes = kTile * D * 2;
+    static constexpr int kStages = D == 128 ? 2 : 4;
+    static constexpr int kRing = 2 * kTileBytes;                       // after the two resident tiles
+    static constexpr int kVec = kRing + kStages * 2 * kTileBytes;      // -lse log2 e and D of a stage's rows
+    static constexpr int kBars = kVec + kStages * 2 * kTile * 4;
+    static constexpr int kBytes = kBars + 256;
+};
+
+// A block's barriers.
+template <int NS>
+struct Bars {
+    uint64_t res_full;     // the resident tiles
+    uint64_t s_full[2];    // scores (of even, odd steps)
+    uint64_t dp_full;      // dO . v
+    uint64_t p_full;       // p written (8 warps)
+    uint64_t ds_full;      // ds written (8 warps)
+    uint64_t acc_done;     // a step's last product
+    uint64_t final_done;   // the last step's
+    uint64_t full[NS], empty[NS];
+    uint64_t tail_bar;
+    uint32_t tmem_slot;
+};
+
+template <int NS>
+__device__ __forceinline__ void init_bars(Bars<NS>* b) {
+    mbar_init(&b->res_full, 1);
+    mbar_init(b->s_full, 1);
+    mbar_init(b->s_full + 1, 1);
+    mbar_init(&b->dp_full, 1);
+    mbar_init(&b->p_full, 8);
+    mbar_init(&b->ds_full, 8);
+    mbar_init(&b->acc_done, 1);
+    mbar_init(&b->final_done, 1);
+    for (int i = 0; i < NS; ++i) {
+        mbar_init(b->full + i, 2);
+        mbar_init(b->empty + i, 1);
+    }
+    mbar_init(&b->tail_bar, 1);
+    fence_barrier_init();
+}
+
+// Whole-warp bounded wait.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity) {
+    return __all_sync(0xffffffffu, mbar_wait(bar, parity)) != 0;
+}
+
+// Loads one pair of tiles (rows `rows` of 128 belong to the sequence) into a stage: both
+// tiles count on `full`, once the rows behind the sequence's end are zero (their weight is
+// zero, which a NaN or an infinity of a neighbouring sequence would survive).  The second of
+// full's two arrivals is the caller's.  One warp; false if a wait ran out.
+template <int D>
+__device__ __forceinline__ bool load_pair(unsigned char* dst, const CUtensorMap* ma, const CUtensorMap* mb,
+                                          int head, int token, int rows, uint64_t* full, uint64_t* tail_bar,
+                                          uint32_t& tail_phase) {
+    constexpr int TB = kTile * D * 2;
+    const bool tail = rows < kTile;
+    uint64_t* bar = tail ? tail_bar : full;
+    if ((threadIdx.x & 31) == 0) {
+        mbar_arrive_expect_tx(bar, 2 * TB);
+        load_tile<D>(dst, ma, head, token, bar);
+        load_tile<D>(dst + TB, mb, head, token, bar);
+    }
+    __syncwarp();
+    if (tail) {
+        if (!warp_wait(tail_bar, tail_phase & 1)) return false;
+        ++tail_phase;
+        zero_rows<D>(dst, rows);
+        zero_rows<D>(dst + TB, rows);
+        if ((threadIdx.x & 31) == 0) mbar_arrive(full);
+    }
+    return true;
+}
+
+// 128 lanes x D columns of tensor memory, times f, as bf16 rows of a token-major tensor
+// [rows][heads][D], through a tile of shared memory that nothing reads any more.  Four warps
+// (`wg` = 0 or 1 picks which of the block's two groups), rows < `rows` only.
+template <int D>
+__device__ __forceinline__ void store_rows(uint32_t tsrc, float f, bool any, unsigned char* tile,
+                                           __nv_bfloat16* dst, long long ld, int rows) {
+    const int w = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31, r = 32 * w + lane;
+    const uint32_t lane0 = (uint32_t)w << 21;
+#pragma unroll
+    for (int x = 0; x < D; x += 32) {
+        float v[32];
+        if (any) {
+            tmem_ld32(tsrc + lane0 + x, v);
+            tmem_wait_ld();
+        } else {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] = 0.f;
+        }
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] *= f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) st_chunk16<true>(tile, r, x / 8 + i, v + 8 * i);
+    }
+    __syncwarp();
+    constexpr int CH = D / 8;
+    for (int i = lane; i < 32 * CH; i += 32) {
+        const int rr = 32 * w + i / CH, ch = i % CH;
+        if (rr < rows)
+            *reinterpret_cast<uint4*>(dst + (long long)rr * ld + 8 * ch) =
+                *reinterpret_cast<const uint4*>(tile + t16_off(rr, ch));
+    }
+}
+
+// dk and dv of 128 keys of one key head: rows of the products are keys, columns queries.
+//
+// S of a step sits in one half of 256 columns, P in the other; p and ds overwrite S, and the
+// next step's S goes to where P was, as soon as ds is formed -- so that the exponentials of
+// the next step run beside this step's last products.
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1) k_attn_dkv(const __grid_constant__ BwdParams p) {
+    using SM = BwdSmem<D>;
+    constexpr int NS = SM::kStages;
+    extern __shared__ __align__(1024) unsigned char sm[];
+    Bars<NS>* bar = reinterpret_cast<Bars<NS>*>(sm + SM::kBars);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int blk = blockIdx.x / p.Hk, hk = blockIdx.x % p.Hk;
+    const Seq sq = p.seq[find_seq(p.seq, p.n, blk)];
+    const int kb = blk - sq.block0;  // with a causal mask the first keys are seen most
+    const int G = p.Hq / p.Hk;
+    const int off = sq.lk - sq.lq;
+    const int k0 = kb * kTile;
+
+    // query tiles [lo, hi) that see any of the block's keys, for each head of the group
+    int lo = 0, hi = (sq.lq + kTile - 1) / kTile;
+    if (p.causal) lo = max(0, k0 - off) / kTile;
+    if (p.window) {
+        const int last = min(k0 + kTile, sq.lk) - 1 + p.window - off - 1;
+        hi = last < 0 ? 0 : min(hi, last / kTile + 1);
+    }
+    const int per = max(0, hi - lo), steps = per * G;
+
+    if (threadIdx.x == 0) init_bars(bar);
+    if (warp == 8) tmem_alloc(&bar->tmem_slot, 512);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = bar->tmem_slot;
+    const uint32_t tV = tmem + 256u, tK = tmem + 256u + (uint32_t)D;
+    float* vec = reinterpret_cast<float*>(sm + SM::kVec);
+
+    if (warp == 9) {
+        // ---------------------------------------------------------------- loads
+        bool ok = true;
+        uint32_t tails = 0;
+        if (lane == 0 && steps > 0) {
+            mbar_arrive_expect_tx(&bar->res_full, 2 * SM::kTileBytes);
+            load_tile<D>(sm, &p.tk, hk, sq.k0 + k0, &bar->res_full);
+            load_tile<D>(sm + SM::kTileBytes, &p.tv, hk, sq.k0 + k0, &bar->res_full);
+        }
+        for (int i = 0; i < steps && ok; ++i) {
+            const int st = i % NS, h = hk * G + i / per, i0 = (lo + i % per) * kTile;
+            if (i >= NS) ok = warp_wait(bar->empty + st, (i / NS - 1) & 1);
+            if (!ok) break;
+            ok = load_pair<D>(sm + SM::kRing + st * 2 * SM::kTileBytes, &p.tq, &p.tdo, h, sq.q0 + i0, sq.lq - i0,
+                              bar->full + st, &bar->tail_bar, tails);
+            // -lse log2 e and D of the tile's queries; -infinity (no weight at all) for rows
+            // that do not exist and for queries that see no key
+            float* v = vec + st * 2 * kTile;
+            const long long at = sq.q0 * p.lse_seq + h * p.lse_head + i0;
+#pragma unroll
+            for (int x = lane; x < kTile; x += 32) {
+                float a = -INFINITY, b = 0.f;
+                if (i0 + x < sq.lq) {
+                    const float e = p.lse[at + x];
+                    a = e == -INFINITY ? -INFINITY : -e * kLog2e;
+                    b = p.delta[at + x];
+                }
+                v[x] = a;
+                v[kTile + x] = b;
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar->full + st);
+        }
+        if (!ok && lane == 0) atomicOr(&g_bwd_timeouts, 1u);
+    } else if (warp == 8) {
+        // ---------------------------------------------------------------- products
+        if (lane == 0 && steps > 0) {
+            constexpr uint32_t id_s = idesc(kBF16, 128, 128, false, false);
+            constexpr uint32_t id_a = idesc(kBF16, 128, D, false, true);
+            const uint32_t ka = saddr(sm), va = saddr(sm + SM::kTileBytes);
+            auto q_of = [&](int j) { return saddr(sm + SM::kRing + (j % NS) * 2 * SM::kTileBytes); };
+            auto scores = [&](int j) {  // S of step j: K Q^T
+                const uint32_t b = q_of(j), d = tmem + (uint32_t)(j & 1) * 128u;
+#pragma unroll
+                for (int k = 0; k < D; k += 16) mma_f16(d, kdesc16(ka, 0, k), kdesc16(b, 0, k), id_s, k ? 1u : 0u);
+                mma_commit(bar->s_full + (j & 1));
+            };
+            auto dots = [&](int j) {  // P of step j: V dO^T
+                const uint32_t b = q_of(j) + SM::kTileBytes, d = tmem + (uint32_t)(1 - (j & 1)) * 128u;
+#pragma unroll
+                for (int k = 0; k < D; k += 16) mma_f16(d, kdesc16(va, 0, k), kdesc16(b, 0, k), id_s, k ? 1u : 0u);
+                mma_commit(&bar->dp_full);
+            };
+            bool ok = mbar_wait(&bar->res_full, 0) && mbar_wait(bar->full, 0);
+            tc_fence_after();
+            if (ok) {
+                scores(0);
+                dots(0);
+            }
+            for (int j = 0; j < steps && ok; ++j) {
+                const uint32_t x = tmem + (uint32_t)(j & 1) * 128u;
+                const uint32_t qa = q_of(j), doa = qa + SM::kTileBytes;
+                ok = mbar_wait(&bar->p_full, j & 1);
+                if (!ok) break;
+                tc_fence_after();
+#pragma unroll
+                for (int k = 0; k < kTile; k += 16)  // p: columns 0-31 of each half of S
+                    mma_f16_ta(tV, x + (k & 64) + (k & 63) / 2, mdesc16(doa, k, 0), id_a, (j || k) ? 1u : 0u);
+                ok = mbar_wait(&bar->ds_full, j & 1);
+                if (!ok) break;
+                tc_fence_after();
+                const bool more = j + 1 < steps;
+                if (more) {
+                    ok = mbar_wait(bar->full + (j + 1) % NS, ((j + 1) / NS) & 1);
+                    if (!ok) break;
+                    tc_fence_after();
+                    scores(j + 1);
+                }
+#pragma unroll
+                for (int k = 0; k < kTile; k += 16)  // ds: columns 32-63 of each half of S
+                    mma_f16_ta(tK, x + 32 + (k & 64) + (k & 63) / 2, mdesc16(qa, k, 0), id_a, (j || k) ? 1u : 0u);
+                if (j + NS < steps) mma_commit(bar->empty + j % NS);
+                if (more) {
+                    mma_commit(&bar->acc_done);
+                    ok = mbar_wait(&bar->acc_done, j & 1);  // before P of j + 1 overwrites p and ds
+                    if (!ok) break;
+                    dots(j + 1);
+                } else {
+                    mma_commit(&bar->final_done);
+                }
+            }
+            if (!ok) atomicOr(&g_bwd_timeouts, 2u);
+        }
+    } else {
+        // ---------------------------------------------------------------- p, ds
+        const int wg = warp >> 2;
+        const uint32_t lane0 = (uint32_t)(warp & 3) << 21;
+        const int key = k0 + (threadIdx.x & 127);  // the thread's row
+        const float c = p.scale_log2;
+        bool ok = true;
+        for (int j = 0; j < steps && ok; ++j) {
+            const uint32_t x = tmem + lane0 + (uint32_t)(j & 1) * 128u + 64u * wg;
+            const uint32_t y = tmem + lane0 + (uint32_t)(1 - (j & 1)) * 128u + 64u * wg;
+            const float4* nl = reinterpret_cast<const float4*>(vec + (j % NS) * 2 * kTile + 64 * wg);
+            const float4* dl = nl + kTile / 4;
+            const int i0 = (lo + j % per) * kTile;
+            // visible columns [a, b) of the thread's 64
+            int a = 0, b = 64;
+            const bool mask = (p.causal && i0 + off < k0 + kTile - 1) || (p.window && i0 + kTile - 1 + off - p.window >= k0);
+            if (mask) {
+                const int first = key - off - i0 - 64 * wg;
+                if (p.causal) a = first;
+                if (p.window) b = min(b, first + p.window);
+            }
+            ok = warp_wait(bar->s_full + (j & 1), (j >> 1) & 1) && warp_wait(bar->full + j % NS, (j / NS) & 1);
+            if (!ok) break;
+            tc_fence_after();
+            float s[2][32];
+            tmem_ld32(x, s[0]);
+            tmem_ld32(x + 32, s[1]);
+            tmem_wait_ld();
+            uint32_t w[32];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                const float4 n = nl[i];
+                float* v = &s[i >> 3][(4 * i) & 31];
+                v[0] = ex2(fmaf(v[0], c, n.x));
+                v[1] = ex2(fmaf(v[1], c, n.y));
+                v[2] = ex2(fmaf(v[2], c, n.z));
+                v[3] = ex2(fmaf(v[3], c, n.w));
+            }
+            if (mask) {
+#pragma unroll
+                for (int i = 0; i < 64; ++i) s[i >> 5][i & 31] = (i >= a && i < b) ? s[i >> 5][i & 31] : 0.f;
+            }
+#pragma unroll
+            for (int i = 0; i < 32; ++i) w[i] = bf16x2(s[i >> 4][(2 * i) & 31], s[i >> 4][(2 * i + 1) & 31]);
+            tmem_st32u(x, w);
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bar->p_full);
+
+            ok = warp_wait(&bar->dp_full, j & 1);
+            if (!ok) break;
+            tc_fence_after();
+#pragma unroll
+            for (int hlf = 0; hlf < 2; ++hlf) {
+                float dp[32];
+                tmem_ld32(y + 32 * hlf, dp);
+                tmem_wait_ld();
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const float4 n = dl[8 * hlf + i];
+                    float* v = &s[hlf][4 * i];
+                    v[0] *= dp[4 * i] - n.x;
+                    v[1] *= dp[4 * i + 1] - n.y;
+                    v[2] *= dp[4 * i + 2] - n.z;
+                    v[3] *= dp[4 * i + 3] - n.w;
+                }
+                if (mask) {  // zero weight times whatever stood there
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) s[hlf][i] = (32 * hlf + i >= a && 32 * hlf + i < b) ? s[hlf][i] : 0.f;
+                }
+#pragma unroll
+                for (int i = 0; i < 16; ++i) w[16 * hlf + i] = bf16x2(s[hlf][2 * i], s[hlf][2 * i + 1]);
+            }
+            tmem_st32u(x + 32, w);
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bar->ds_full);
+        }
+        if (steps > 0 && ok) {
+            ok = warp_wait(&bar->final_done, 0);
+            tc_fence_after();
+        }
+        if (!ok && lane == 0) atomicOr(&g_bwd_timeouts, 4u);
+        const long long ld = (long long)p.Hk * D, at = (long long)(sq.k0 + k0) * ld + hk * D;
+        if (wg == 0) store_rows<D>(tK, p.scale, steps > 0, sm, p.dk + at, ld, sq.lk - k0);
+        else store_rows<D>(tV, 1.f, steps > 0, sm + SM::kTileBytes, p.dv + at, ld, sq.lk - k0);
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 8) {
+        __syncwarp();
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+// dq of 128 queries of one head: rows of the products are queries, columns keys.  The scores
+// alternate between two places, so that a step's are formed while the step before is still
+// at its exponentials.
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1) k_attn_dq(const __grid_constant__ BwdParams p) {
+    using SM = BwdSmem<D>;
+    constexpr int NS = SM::kStages;
+    extern __shared__ __align__(1024) unsigned char sm[];
+    Bars<NS>* bar = reinterpret_cast<Bars<NS>*>(sm + SM::kBars);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int blk = blockIdx.x / p.Hq, h = blockIdx.x % p.Hq;
+    const Seq sq = p.seq[find_seq(p.seq, p.n, blk)];
+    const int nblk = (sq.lq + kTile - 1) / kTile;
+    const int qb = nblk - 1 - (blk - sq.block0);
+    const int hk = h / (p.Hq / p.Hk);
+    const int off = sq.lk - sq.lq;
+    const int r0 = qb * kTile, r1 = min(r0 + kTile, sq.lq) - 1;
+
+    int last = sq.lk - 1, first = 0;
+    if (p.causal) last = min(last, r1 + off);
+    if (p.window) first = max(first, r0 + off - p.window + 1);
+    const int lo = first / kTile;
+    const int steps = last < first ? 0 : last / kTile + 1 - lo;
+
+    if (threadIdx.x == 0) init_bars(bar);
+    if (warp == 8) tmem_alloc(&bar->tmem_slot, 512);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = bar->tmem_slot;
+    const uint32_t tP = tmem + 256u, tQ = tmem + 384u;
+
+    if (warp == 9) {
+        bool ok = true;
+        uint32_t tails = 0;
+        if (lane == 0 && steps > 0) {
+            mbar_arrive_expect_tx(&bar->res_full, 2 * SM::kTileBytes);
+            load_tile<D>(sm, &p.tq, h, sq.q0 + r0, &bar->res_full);
+            load_tile<D>(sm + SM::kTileBytes, &p.tdo, h, sq.q0 + r0, &bar->res_full);
+        }
+        for (int i = 0; i < steps && ok; ++i) {
+            const int st = i % NS, j0 = (lo + i) * kTile;
+            if (i >= NS) ok = warp_wait(bar->empty + st, (i / NS - 1) & 1);
+            if (!ok) break;
+            ok = load_pair<D>(sm + SM::kRing + st * 2 * SM::kTileBytes, &p.tk, &p.tv, hk, sq.k0 + j0, sq.lk - j0,
+                              bar->full + st, &bar->tail_bar, tails);
+            if (lane == 0) mbar_arrive(bar->full + st);
+        }
+        if (!ok && lane == 0) atomicOr(&g_bwd_timeouts, 8u);
+    } else if (warp == 8) {
+        if (lane == 0 && steps > 0) {
+            constexpr uint32_t id_s = idesc(kBF16, 128, 128, false, false);
+            constexpr uint32_t id_a = idesc(kBF16, 128, D, false, true);
+            const uint32_t qa = saddr(sm), doa = saddr(sm + SM::kTileBytes);
+            auto k_of = [&](int j) { return saddr(sm + SM::kRing + (j % NS) * 2 * SM::kTileBytes); };
+            auto scores = [&](int j) {  // Q K^T
+                const uint32_t b = k_of(j), d = tmem + (uint32_t)(j & 1) * 128u;
+#pragma unroll
+                for (int k = 0; k < D; k += 16) mma_f16(d, kdesc16(qa, 0, k), kdesc16(b, 0, k), id_s, k ? 1u : 0u);
+                mma_commit(bar->s_full + (j & 1));
+            };
+            auto dots = [&](int j) {  // dO V^T
+                const uint32_t b = k_of(j) + SM::kTileBytes;
+#pragma unroll
+                for (int k = 0; k < D; k += 16) mma_f16(tP, kdesc16(doa, 0, k), kdesc16(b, 0, k), id_s, k ? 1u : 0u);
+                mma_commit(&bar->dp_full);
+            };
+            bool ok = mbar_wait(&bar->res_full, 0) && mbar_wait(bar->full, 0);
+            tc_fence_after();
+            if (ok) {
+                scores(0);
+                dots(0);
+            }
+            for (int j = 0; j < steps && ok; ++j) {
+                const bool more = j + 1 < steps;
+                if (more) {
+                    ok = mbar_wait(bar->full + (j + 1) % NS, ((j + 1) / NS) & 1);
+                    // the scores' other place is free once step j - 1's ds there has been used
+                    if (ok && j > 0) ok = mbar_wait(&bar->acc_done, (j - 1) & 1);
+                    if (!ok) break;
+                    tc_fence_after();
+                    scores(j + 1);
+                }
+                ok = mbar_wait(&bar->ds_full, j & 1);
+                if (!ok) break;
+                tc_fence_after();
+                if (more) dots(j + 1);
+                const uint32_t x = tmem + (uint32_t)(j & 1) * 128u, b = k_of(j);
+#pragma unroll
+                for (int k = 0; k < kTile; k += 16)  // ds: columns 0-31 of each half of S
+                    mma_f16_ta(tQ, x + (k & 64) + (k & 63) / 2, mdesc16(b, k, 0), id_a, (j || k) ? 1u : 0u);
+                if (j + NS < steps) mma_commit(bar->empty + j % NS);
+                if (j + 2 < steps) mma_commit(&bar->acc_done);
+                if (!more) mma_commit(&bar->final_done);
+            }
+            if (!ok) atomicOr(&g_bwd_timeouts, 16u);
+        }
+    } else {
+        const int wg = warp >> 2;
+        const uint32_t lane0 = (uint32_t)(warp & 3) << 21;
+        const int row = r0 + (threadIdx.x & 127);
+        const int at = row + off;
+        const int kmax = p.causal ? min(sq.lk - 1, at) : sq.lk - 1;
+        const int kmin = p.window ? at - p.window + 1 : 0;
+        const int all_max = p.causal ? min(sq.lk - 1, r0 + off) : sq.lk - 1;
+        const int all_min = p.window ? r0 + kTile - 1 + off - p.window + 1 : 0;
+        float nl = -INFINITY, dl = 0.f;  // rows that do not exist and queries that see no key: no weight
+        if (row < sq.lq) {
+            const long long v = sq.q0 * p.lse_seq + h * p.lse_head + row;
+            const float e = p.lse[v];
+            if (e != -INFINITY) nl = -e * kLog2e;
+            dl = p.delta[v];
+        }
+        const float c = p.scale_log2;
+        bool ok = true;
+        for (int j = 0; j < steps && ok; ++j) {
+            const uint32_t x = tmem + lane0 + (uint32_t)(j & 1) * 128u + 64u * wg;
+            const int j0 = (lo + j) * kTile;
+            const bool mask = j0 + kTile - 1 > all_max || j0 < all_min;
+            const int a = kmin - j0 - 64 * wg, b = kmax - j0 - 64 * wg;
+            ok = warp_wait(bar->s_full + (j & 1), (j >> 1) & 1);
+            if (!ok) break;
+            tc_fence_after();
+            float s[2][32];
+            tmem_ld32(x, s[0]);
+            tmem_ld32(x + 32, s[1]);
+            tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 64; ++i) s[i >> 5][i & 31] = ex2(fmaf(s[i >> 5][i & 31], c, nl));
+            ok = warp_wait(&bar->dp_full, j & 1);
+            if (!ok) break;
+            tc_fence_after();
+            uint32_t w[32];
+#pragma unroll
+            for (int hlf = 0; hlf < 2; ++hlf) {
+                float dp[32];
+                tmem_ld32(tP + lane0 + 64 * wg + 32 * hlf, dp);
+                tmem_wait_ld();
+#pragma unroll
+                for (int i = 0; i < 32; ++i) s[hlf][i] *= dp[i] - dl;
+                if (mask) {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) s[hlf][i] = (32 * hlf + i >= a && 32 * hlf + i <= b) ? s[hlf][i] : 0.f;
+                }
+#pragma unroll
+                for (int i = 0; i < 16; ++i) w[16 * hlf + i] = bf16x2(s[hlf][2 * i], s[hlf][2 * i + 1]);
+            }
+            tmem_st32u(x, w);
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bar->ds_full);
+        }
+        if (steps > 0 && ok) {
+            ok = warp_wait(&bar->final_done, 0);
+            tc_fence_after();
+        }
+        if (!ok && lane == 0) atomicOr(&g_bwd_timeouts, 32u);
+        const long long ld = (long long)p.Hq * D;
+        if (wg == 0)
+            store_rows<D>(tQ, p.scale, steps > 0, sm, p.dq + (long long)(sq.q0 + r0) * ld + h * D, ld, sq.lq - r0);
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 8) {
+        __syncwarp();
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+template <int D>
+cudaError_t run(const Problem& p, BwdParams& a, const void* o, const void* dO, float* delta, cudaStream_t st) {
+    cudaError_t err = cudaFuncSetAttribute(k_attn_dkv<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, BwdSmem<D>::kBytes);
+    if (err == cudaSuccess)
+        err = cudaFuncSetAttribute(k_attn_dq<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, BwdSmem<D>::kBytes);
+    if (err != cudaSuccess) return err;
+    if (p.q_rows > 0) {
+        const long long rows = p.q_rows * p.Hq;
+        constexpr int kRowsPerBlock = 8 * (32 / (D / 8));
+        MUIR_TIMED("k_attn_delta", st,
+                   k_attn_delta<D><<<(unsigned)((rows + kRowsPerBlock - 1) / kRowsPerBlock), 256, 0, st>>>(
+                       static_cast<const __nv_bfloat16*>(o), static_cast<const __nv_bfloat16*>(dO), delta, rows,
+                       p.Hq, p.Tq, p.lse_seq, p.lse_head));
+        if ((err = cudaGetLastError()) != cudaSuccess) return err;
+    }
+    long long blocks;
+    for (int i = 0; i < p.n;) {
+        a.n = gather_seqs(p, i, true, kTile, a.seq, &i, &blocks);
+        if (a.n == 0) continue;
+        MUIR_TIMED("k_attn_dkv", st,
+                   k_attn_dkv<D><<<(unsigned)(blocks * p.Hk), kThreads, BwdSmem<D>::kBytes, st>>>(a));
+        if ((err = cudaGetLastError()) != cudaSuccess) return err;
+    }
+    for (int i = 0; i < p.n;) {
+        a.n = gather_seqs(p, i, false, kTile, a.seq, &i, &blocks);
+        if (a.n == 0) continue;
+        MUIR_TIMED("k_attn_dq", st,
+                   k_attn_dq<D><<<(unsigned)(blocks * p.Hq), kThreads, BwdSmem<D>::kBytes, st>>>(a));
+        if ((err = cudaGetLastError()) != cudaSuccess) return err;
+    }
+    return cudaSuccess;
+}
+
+}  // namespace
+
+size_t bwd_ws_bytes(const Problem& p) { return (size_t)p.q_rows * p.Hq * 4; }
+
+cudaError_t run_bwd(const Problem& p, const void* o, const float* lse, const void* dO, void* dq, void* dk,
+                    void* dv, void* ws, cudaStream_t st) {
+    BwdParams a;
+    cudaError_t err = cudaSuccess;
+    if (p.q_rows > 0) {
+        err = make_tmap_tokens(&a.tq, p.q, p.d, p.Hq, p.q_ld, p.q_rows, kTile);
+        if (err == cudaSuccess)
+            err = make_tmap_tokens(&a.tdo, dO, p.d, p.Hq, (long long)p.Hq * p.d, p.q_rows, kTile);
+    }
+    if (err == cudaSuccess && p.k_rows > 0) {
+        err = make_tmap_tokens(&a.tk, p.k, p.d, p.Hk, p.k_ld, p.k_rows, kTile);
+        if (err == cudaSuccess) err = make_tmap_tokens(&a.tv, p.v, p.d, p.Hk, p.v_ld, p.k_rows, kTile);
+    }
+    if (err != cudaSuccess) return err;
+    a.lse = lse;
+    a.delta = static_cast<float*>(ws);
+    a.dq = static_cast<__nv_bfloat16*>(dq);
+    a.dk = static_cast<__nv_bfloat16*>(dk);
+    a.dv = static_cast<__nv_bfloat16*>(dv);
+    a.lse_seq = p.lse_seq;
+    a.lse_head = p.lse_head;
+    a.scale = p.scale;
+    a.scale_log2 = p.scale * kLog2e;
+    a.Hq = p.Hq; a.Hk = p.Hk; a.causal = p.causal; a.window = p.window;
+    return p.d == 128 ? run<128>(p, a, o, dO, static_cast<float*>(ws), st)
+                      : run<64>(p, a, o, dO, static_cast<float*>(ws), st);
+}
+
+unsigned int timeouts_bwd() {
+    unsigned int n = 0;
+    cudaMemcpyFromSymbol(&n, g_bwd_timeouts, sizeof(n));
+    const unsigned int z = 0;
+    cudaMemcpyToSymbol(g_bwd_timeouts, &z, sizeof(z));
+    return n;
+}
+
+}  // namespace attn
+}  // namespace muir

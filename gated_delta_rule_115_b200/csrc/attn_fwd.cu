@@ -1,0 +1,418 @@
+// attn_fwd.cu -- softmax attention, forward, on tcgen05.
+//
+//     s_ij = scale q_i . k_j,   lse_i = log sum_j exp s_ij,   o_i = sum_j exp(s_ij - lse_i) v_j
+//
+// over the keys j that query i sees: j <= i + lk - lq (causal), j > i + lk - lq - window.
+//
+// One block takes two tiles of 128 queries of one head of one sequence and walks the keys in
+// tiles of 128 once, with the running maximum and sum of each row (base 2, float32).  The
+// score product lands in tensor memory, four warps a tile turn it into weights -- a row to a
+// thread, so that no row is reduced across threads -- and write them back over the scores as
+// the A operand of the second product, whose sum stays in tensor memory until the end.  The
+// two tiles run half a step apart: while the threads of one work on its exponentials, the
+// tensor cores run the products of the other.
+//
+//   warps 0-3, 4-7 : softmax of tile 0, 1     warp 8 : issues every product
+//   warp 9         : loads (TMA, a ring of key and value tiles)
+//
+// The maximum that the weights are taken against moves only when a row outgrows it by 2^8:
+// weights up to 2^8 lose nothing in bf16, and the sum in tensor memory is rescaled a few
+// times a row instead of at every step.  Weights are rounded to bf16 (half a step, 2^-8) as
+// the product's operands; the sums are of the unrounded ones, in float32.
+//
+// Bound by the tensor cores (4 d flops a visible pair) and, at d = 64 before anything else,
+// by the exponentials (16 a clock and SM).
+#include <algorithm>
+
+#include "attn_dev.cuh"
+#include "profile.h"
+#include "tmap.h"
+
+namespace muir {
+namespace attn {
+
+__device__ unsigned int g_fwd_timeouts;
+
+namespace {
+
+constexpr int kThreads = 320;
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kSlack = 8.f;  // log2 of how far a weight may exceed 1
+
+struct FwdParams {
+    CUtensorMap tq, tk, tv;
+    __nv_bfloat16* o;
+    float* lse;
+    long long lse_seq, lse_head;
+    float scale_log2;
+    int Hq, Hk, causal, window, n;
+    Seq seq[kMaxSeqs];
+};
+
+template <int D>
+struct FwdSmem {
+    static constexpr int kTileBytes = kTile * D * 2;
+    static constexpr int kStages = D == 128 ? 4 : 8;
+    static constexpr int kRing = 2 * kTileBytes;
+    static constexpr int kBars = kRing + kStages * kTileBytes;
+    static constexpr int kBytes = kBars + 256;
+};
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1) k_attn_fwd(const __grid_constant__ FwdParams p) {
+    using SM = FwdSmem<D>;
+    constexpr int NS = SM::kStages;
+    extern __shared__ __align__(1024) unsigned char sm[];
+    uint64_t* q_full = reinterpret_cast<uint64_t*>(sm + SM::kBars);
+    uint64_t* s_full = q_full + 2;     // scores of a tile's step are in tensor memory
+    uint64_t* p_full = s_full + 2;     // its weights are
+    uint64_t* pv_done = p_full + 2;    // its second product has finished
+    uint64_t* kv_full = pv_done + 2;
+    uint64_t* kv_empty = kv_full + NS;
+    uint64_t* tail_bar = kv_empty + NS;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tail_bar + 1);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int blk = blockIdx.x / p.Hq, h = blockIdx.x % p.Hq;
+    const Seq sq = p.seq[find_seq(p.seq, p.n, blk)];
+    // the longest rows of a causal sequence first
+    const int nblk = (sq.lq + 2 * kTile - 1) / (2 * kTile);
+    const int qb = nblk - 1 - (blk - sq.block0);
+    const int hk = h / (p.Hq / p.Hk);
+    const int off = sq.lk - sq.lq;
+
+    // key tiles [lo, hi) of each of the two query tiles
+    int lo[2], hi[2];
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+        const int r0 = (2 * qb + t) * kTile, r1 = min(r0 + kTile, sq.lq) - 1;  // its rows [r0, r1]
+        int last = sq.lk - 1, first = 0;
+        if (p.causal) last = min(last, r1 + off);
+        if (p.window) first = max(first, r0 + off - p.window + 1);
+        hi[t] = last < 0 ? 0 : last / kTile + 1;
+        lo[t] = first / kTile;
+        if (r0 >= sq.lq || last < first) hi[t] = lo[t] = 0;
+    }
+    const bool on0 = hi[0] > lo[0], on1 = hi[1] > lo[1];
+    const int jlo = on0 ? (on1 ? min(lo[0], lo[1]) : lo[0]) : lo[1];
+    const int jhi = on0 ? (on1 ? max(hi[0], hi[1]) : hi[0]) : hi[1];
+    const int loads = 2 * (jhi - jlo);  // K, V of each key tile in turn
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(q_full + i, 1);
+            mbar_init(s_full + i, 1);
+            mbar_init(p_full + i, 4);
+            mbar_init(pv_done + i, 1);
+        }
+        for (int i = 0; i < NS; ++i) {
+            mbar_init(kv_full + i, 1);
+            mbar_init(kv_empty + i, 1);
+        }
+        mbar_init(tail_bar, 1);
+        fence_barrier_init();
+    }
+    if (warp == 8) tmem_alloc(tmem_slot, 512);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    const uint32_t tS[2] = {tmem, tmem + 128u}, tO[2] = {tmem + 256u, tmem + 256u + (uint32_t)D};
+    bool bad = false;
+
+    if (warp == 9) {
+        // ---------------------------------------------------------------- loads
+        if (lane == 0) {
+            for (int t = 0; t < 2; ++t)
+                if (hi[t] > lo[t]) {
+                    mbar_arrive_expect_tx(q_full + t, SM::kTileBytes);
+                    load_tile<D>(sm + t * SM::kTileBytes, &p.tq, h, sq.q0 + (2 * qb + t) * kTile, q_full + t);
+                }
+        }
+        for (int i = 0; i < loads; ++i) {
+            const int st = i % NS, j = jlo + i / 2;
+            if (i >= NS) {
+                const bool ok = mbar_wait(kv_empty + st, (i / NS - 1) & 1);
+                if (!__all_sync(0xffffffffu, ok)) {
+                    bad = true;
+                    break;
+                }
+            }
+            unsigned char* dst = sm + SM::kRing + st * SM::kTileBytes;
+            const int rows = sq.lk - j * kTile;
+            // The value rows behind the sequence's last key belong to another sequence or to
+            // nobody: their weight is zero, which a NaN or an infinity there would survive.
+            const bool tail = (i & 1) && rows < kTile;
+            uint64_t* bar = tail ? tail_bar : kv_full + st;
+            if (lane == 0) {
+                mbar_arrive_expect_tx(bar, SM::kTileBytes);
+                load_tile<D>(dst, (i & 1) ? &p.tv : &p.tk, hk, sq.k0 + j * kTile, bar);
+            }
+            __syncwarp();
+            if (tail) {
+                const bool ok = mbar_wait(tail_bar, 0);
+                if (!__all_sync(0xffffffffu, ok)) {
+                    bad = true;
+                    break;
+                }
+                zero_rows<D>(dst, rows);
+                if (lane == 0) mbar_arrive(kv_full + st);
+            }
+        }
+        if (bad && lane == 0) atomicOr(&g_fwd_timeouts, 1u);
+    } else if (warp == 8) {
+        // ---------------------------------------------------------------- products
+        if (lane == 0 && loads > 0) {
+            constexpr uint32_t id_s = idesc(kBF16, 128, 128, false, false);
+            constexpr uint32_t id_o = idesc(kBF16, 128, D, false, true);
+            int ns[2] = {lo[0], lo[1]};  // next score product of each tile
+            int np[2] = {lo[0], lo[1]};  // next output product
+            uint64_t t0 = globaltimer();
+            int idle = 0;
+            while (np[0] < hi[0] || np[1] < hi[1]) {
+                bool moved = false;
+#pragma unroll
+                for (int t = 0; t < 2; ++t) {
+                    if (ns[t] < hi[t] && ns[t] == np[t]) {
+                        // the scores' place is free once the weights there have been used
+                        const int j = ns[t], i = 2 * (j - jlo), st = i % NS;
+                        if ((j == lo[t] ? mbar_test(q_full + t, 0) : mbar_test(pv_done + t, (j - 1 - lo[t]) & 1)) &&
+                            mbar_test(kv_full + st, (i / NS) & 1)) {
+                            tc_fence_after();
+                            const uint32_t a = saddr(sm + t * SM::kTileBytes);
+                            const uint32_t b = saddr(sm + SM::kRing + st * SM::kTileBytes);
+#pragma unroll
+                            for (int k = 0; k < D; k += 16)
+                                mma_f16(tS[t], kdesc16(a, 0, k), kdesc16(b, 0, k), id_s, k ? 1u : 0u);
+                            mma_commit(s_full + t);
+                            ns[t] = j + 1;
+                            const int u = 1 - t;
+                            if ((j < lo[u] || j >= hi[u] || ns[u] > j) && i + NS < loads) mma_commit(kv_empty + st);
+                            moved = true;
+                        }
+                    } else if (ns[t] > np[t]) {
+                        const int j = np[t], i = 2 * (j - jlo) + 1, st = i % NS;
+                        if (mbar_test(p_full + t, (j - lo[t]) & 1) && mbar_test(kv_full + st, (i / NS) & 1)) {
+                            tc_fence_after();
+                            const uint32_t b = saddr(sm + SM::kRing + st * SM::kTileBytes);
+#pragma unroll
+                            for (int k = 0; k < kTile; k += 16)
+                                mma_f16_ta(tO[t], tS[t] + k / 2, mdesc16(b, k, 0), id_o, (j > lo[t] || k) ? 1u : 0u);
+                            mma_commit(pv_done + t);
+                            np[t] = j + 1;
+                            const int u = 1 - t;
+                            if ((j < lo[u] || j >= hi[u] || np[u] > j) && i + NS < loads) mma_commit(kv_empty + st);
+                            moved = true;
+                        }
+                    }
+                }
+                if (moved) {
+                    idle = 0;
+                } else if ((++idle & 1023) == 0) {
+                    if (idle == 1024) t0 = globaltimer();
+                    else if (globaltimer() - t0 > kWaitNs) {
+                        atomicOr(&g_fwd_timeouts, 2u);
+                        break;
+                    }
+                }
+            }
+        }
+    } else {
+        // ---------------------------------------------------------------- softmax
+        const int t = warp >> 2;
+        const int row = (2 * qb + t) * kTile + (threadIdx.x & 127);  // of the sequence
+        const uint32_t lane0 = (uint32_t)(warp & 3) << 21;           // this warp's TMEM lanes
+        const int at = row + off;
+        const int kmax = p.causal ? min(sq.lk - 1, at) : sq.lk - 1;  // visible keys [kmin, kmax]
+        const int kmin = p.window ? at - p.window + 1 : 0;
+        // of the tile's first and last row: which key tiles need no mask
+        const int r0 = (2 * qb + t) * kTile;
+        const int all_max = p.causal ? min(sq.lk - 1, r0 + off) : sq.lk - 1;
+        const int all_min = p.window ? r0 + kTile - 1 + off - p.window + 1 : 0;
+        float m = -INFINITY, l = 0.f;  // m in units of score * scale * log2 e
+        const float c = p.scale_log2;
+
+        for (int j = lo[t]; j < hi[t]; ++j) {
+            const bool ok = mbar_wait(s_full + t, (j - lo[t]) & 1);
+            if (!__all_sync(0xffffffffu, ok)) {
+                bad = true;
+                break;
+            }
+            tc_fence_after();
+            float s[4][32];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) tmem_ld32(tS[t] + lane0 + 32 * i, s[i]);
+            tmem_wait_ld();
+            const int k0 = j * kTile;
+            if (k0 + kTile - 1 > all_max || k0 < all_min) {
+                const int a = kmin - k0, b = kmax - k0;
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int x = 0; x < 32; ++x)
+                        s[i][x] = (32 * i + x >= a && 32 * i + x <= b) ? s[i][x] : -INFINITY;
+            }
+            float mx[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                mx[i] = fmaxf(s[i][0], s[i][1]);
+#pragma unroll
+                for (int x = 2; x < 32; x += 2) mx[i] = fmaxf(mx[i], fmaxf(s[i][x], s[i][x + 1]));
+            }
+            // largest s * c: the scale may be negative or zero only with the smallest s, so
+            // the callers' scale is required to be positive
+            const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
+            const bool grow = top > m + kSlack || (m == -INFINITY && top > -INFINITY);
+            if (__any_sync(0xffffffffu, grow)) {
+                const float mn = fmaxf(m, top);
+                const float a = mn == -INFINITY ? 1.f : ex2(m - mn);
+                m = mn;
+                l *= a;
+                if (j > lo[t]) {
+#pragma unroll
+                    for (int x = 0; x < D; x += 16) {
+                        float o[16];
+                        tmem_ld16(tO[t] + lane0 + x, o);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) o[i] *= a;
+                        tmem_st16(tO[t] + lane0 + x, o);
+                    }
+                }
+            }
+            const float neg = m == -INFINITY ? 0.f : -m;
+            float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                uint32_t w[32];
+#pragma unroll
+                for (int x = 0; x < 32; ++x) {
+                    const float e0 = ex2(fmaf(s[2 * i + (x >> 4)][(2 * x) & 31], c, neg));
+                    const float e1 = ex2(fmaf(s[2 * i + (x >> 4)][(2 * x + 1) & 31], c, neg));
+                    sum[x & 1] += e0;
+                    sum[2 + (x & 1)] += e1;
+                    w[x] = bf16x2(e0, e1);
+                }
+                tmem_st32u(tS[t] + lane0 + 32 * i, w);
+            }
+            l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(p_full + t);
+        }
+
+        // ---- the row's sum, scaled; through the tile's query rows (no product reads them any more)
+        const int steps = hi[t] - lo[t];
+        if (steps > 0 && !bad) {
+            const bool ok = mbar_wait(pv_done + t, (steps - 1) & 1);
+            if (!__all_sync(0xffffffffu, ok)) bad = true;
+            tc_fence_after();
+        }
+        if (bad && lane == 0) atomicOr(&g_fwd_timeouts, 4u);
+        const float inv = l == 0.f ? 0.f : 1.f / l;  // no key seen: zero; a NaN stays
+        unsigned char* tile = sm + t * SM::kTileBytes;
+        const int r = threadIdx.x & 127;
+#pragma unroll
+        for (int x = 0; x < D; x += 32) {
+            float o[32];
+            if (steps > 0) {
+                tmem_ld32(tO[t] + lane0 + x, o);
+                tmem_wait_ld();
+            } else {
+#pragma unroll
+                for (int i = 0; i < 32; ++i) o[i] = 0.f;
+            }
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] *= inv;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) st_chunk16<true>(tile, r, x / 8 + i, o + 8 * i);
+        }
+        if (row < sq.lq)
+            p.lse[sq.q0 * p.lse_seq + h * p.lse_head + row] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+        __syncwarp();
+        // each warp stores its 32 rows, D * 2 / 16 lanes a row
+        constexpr int CH = D / 8;
+        for (int i = lane; i < 32 * CH; i += 32) {
+            const int rr = 32 * (warp & 3) + i / CH, ch = i % CH;
+            const int grow = (2 * qb + t) * kTile + rr;
+            if (grow < sq.lq)
+                *reinterpret_cast<uint4*>(p.o + ((long long)(sq.q0 + grow) * p.Hq + h) * D + 8 * ch) =
+                    *reinterpret_cast<const uint4*>(tile + t16_off(rr, ch));
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 8) {
+        __syncwarp();
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+template <int D>
+cudaError_t launch(const FwdParams& a, unsigned blocks, cudaStream_t st) {
+    const cudaError_t err = cudaFuncSetAttribute(k_attn_fwd<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                 FwdSmem<D>::kBytes);
+    if (err != cudaSuccess) return err;
+    MUIR_TIMED("k_attn_fwd", st, k_attn_fwd<D><<<blocks, kThreads, FwdSmem<D>::kBytes, st>>>(a));
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+int gather_seqs(const Problem& p, int first, bool by_keys, int rows_per_block, Seq* out, int* next,
+                long long* blocks) {
+    int n = 0, i = first;
+    for (; i < p.n && n < kMaxSeqs; ++i) {
+        const Seq s = p.seq(i);
+        if ((by_keys ? s.lk : s.lq) > 0) out[n++] = s;
+    }
+    *next = i;
+    std::sort(out, out + n, [by_keys](const Seq& x, const Seq& y) {
+        const int lx = by_keys ? x.lk : x.lq, ly = by_keys ? y.lk : y.lq;
+        return lx != ly ? lx > ly : x.q0 < y.q0;
+    });
+    long long total = 0;
+    for (int k = 0; k < n; ++k) {
+        out[k].block0 = (int)total;
+        total += ((by_keys ? out[k].lk : out[k].lq) + rows_per_block - 1) / rows_per_block;
+    }
+    *blocks = total;
+    return n;
+}
+
+cudaError_t run_fwd(const Problem& p, void* o, float* lse, cudaStream_t st) {
+    FwdParams a;
+    if (p.q_rows == 0) return cudaSuccess;
+    cudaError_t err = make_tmap_tokens(&a.tq, p.q, p.d, p.Hq, p.q_ld, p.q_rows, kTile);
+    if (err == cudaSuccess && p.k_rows > 0) err = make_tmap_tokens(&a.tk, p.k, p.d, p.Hk, p.k_ld, p.k_rows, kTile);
+    if (err == cudaSuccess && p.k_rows > 0) err = make_tmap_tokens(&a.tv, p.v, p.d, p.Hk, p.v_ld, p.k_rows, kTile);
+    if (err != cudaSuccess) return err;
+    a.o = static_cast<__nv_bfloat16*>(o);
+    a.lse = lse;
+    a.lse_seq = p.lse_seq;
+    a.lse_head = p.lse_head;
+    a.scale_log2 = p.scale * kLog2e;
+    a.Hq = p.Hq; a.Hk = p.Hk; a.causal = p.causal; a.window = p.window;
+    for (int i = 0; i < p.n;) {
+        long long blocks;
+        a.n = gather_seqs(p, i, false, 2 * kTile, a.seq, &i, &blocks);
+        if (a.n == 0) continue;
+        err = p.d == 128 ? launch<128>(a, (unsigned)(blocks * p.Hq), st) : launch<64>(a, (unsigned)(blocks * p.Hq), st);
+        if (err != cudaSuccess) return err;
+    }
+    return cudaSuccess;
+}
+
+unsigned int timeouts_fwd() {
+    unsigned int n = 0;
+    cudaMemcpyFromSymbol(&n, g_fwd_timeouts, sizeof(n));
+    const unsigned int z = 0;
+    cudaMemcpyToSymbol(g_fwd_timeouts, &z, sizeof(z));
+    return n;
+}
+
+}  // namespace attn
+}  // namespace muir

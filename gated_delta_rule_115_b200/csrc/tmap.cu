@@ -26,10 +26,18 @@ cudaError_t encode3(CUtensorMap* m, CUtensorMapDataType type, const void* base, 
     const EncodeTiledFn enc = encode_fn();
     if (!enc) return cudaErrorNotSupported;
     const cuuint32_t es[3] = {1, 1, 1};
-    return enc(m, type, 3, const_cast<void*>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
-               swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
-               ? cudaSuccess
-               : cudaErrorInvalidValue;
+    auto encode = [&] {
+        return enc(m, type, 3, const_cast<void*>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                   swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    };
+    if (encode() == CUDA_SUCCESS) return cudaSuccess;
+    // A driver call needs a current context, which a thread that has made no runtime call
+    // yet (an autograd worker's first) does not have: selecting its device makes it current.
+    int dev = 0;
+    cudaError_t err = cudaGetDevice(&dev);
+    if (err == cudaSuccess) err = cudaSetDevice(dev);
+    if (err != cudaSuccess) return err;
+    return encode() == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
 }  // namespace

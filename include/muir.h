@@ -398,6 +398,64 @@ muir_status muir_rotary(int B, int T, int Hq, int Hk, int d, int rot, muir_dtype
                         void* k_out, long long k_out_ld, void* stream);
 
 /*
+ * Softmax attention, for the layers of a stack that mixes it with the gated delta
+ * rule.  Per query head h, whose key head is h / (Hq / Hk), query i and the keys j
+ * that it sees:
+ *
+ *     s_ij = scale q_i . k_j,  lse_i = log sum_j exp s_ij,  o_i = sum_j exp(s_ij - lse_i) v_j
+ *
+ *   visible   : query i stands at position i + Tk - Tq of its sequence's keys
+ *               (queries are the last tokens).  causal: j <= that position;
+ *               window > 0: j > that position - window
+ *   q, dO     : [B][Tq][Hq][d] bfloat16;  k, v : [B][Tk][Hk][d] bfloat16
+ *   *_ld      : elements between tokens of q, k, v (0 = heads * d), so that the three
+ *               may be parts of one projection's rows; multiples of 8
+ *   o, dq     : [B][Tq][Hq][d] bfloat16;  dk, dv : [B][Tk][Hk][d] bfloat16, dense
+ *   lse       : [B][Hq][Tq] float32
+ * A query that sees no key gets o = 0, lse = -inf and no gradient; a key that no query
+ * sees gets zero gradients.  Values of masked keys carry weight zero, not absence: a NaN
+ * or an infinity there can reach queries of its own sequence; none reaches another one.
+ * Arithmetic: products of bfloat16 operands with float32 sums; softmax, lse and row sums
+ * in float32; the weights, and in the backward pass their gradients, are rounded to
+ * bfloat16 as operands of the second product.  Results repeat bit for bit: no atomics.
+ * d is 64 or 128, Hk divides Hq, scale is positive.  Tq or Tk may be 0.  Bound by the
+ * tensor cores: 4 d flops a visible pair forward, 10 d backward.
+ *
+ * muir_attn_bwd: gradients of sum(o * dO).  o and lse are the forward's; the
+ * probabilities are recomputed from lse.  Workspace: one float32 a query and head.
+ *
+ * The varlen forms take num_seqs sequences packed in one buffer, as muir_chunk_fwd_varlen
+ * does: B = 1, Tq and Tk total tokens, cu_q and cu_k HOST arrays of num_seqs + 1 offsets
+ * (cu_k NULL = cu_q); lse is [Hq][Tq].  Sequences may be empty.  One launch for up to
+ * 128 sequences.  Rows of the outputs that belong to no sequence do not exist: the
+ * offsets end at Tq and Tk.
+ */
+typedef struct {
+    int B, Tq, Tk, Hq, Hk, d;
+    int causal;                    /* 0 or 1 */
+    int window;                    /* 0 = none */
+    float scale;
+    long long q_ld, k_ld, v_ld;    /* 0 = dense */
+} muir_attn_shape;
+
+muir_status muir_attn_fwd(const muir_attn_shape* shape, const void* q, const void* k,
+                          const void* v, void* o, float* lse, void* stream);
+size_t muir_attn_bwd_workspace(const muir_attn_shape* shape);
+muir_status muir_attn_bwd(const muir_attn_shape* shape, const void* q, const void* k,
+                          const void* v, const void* o, const float* lse, const void* dO,
+                          void* dq, void* dk, void* dv, void* ws, size_t ws_bytes,
+                          void* stream);
+muir_status muir_attn_fwd_varlen(const muir_attn_shape* shape, int num_seqs,
+                                 const long long* cu_q, const long long* cu_k, const void* q,
+                                 const void* k, const void* v, void* o, float* lse,
+                                 void* stream);
+muir_status muir_attn_bwd_varlen(const muir_attn_shape* shape, int num_seqs,
+                                 const long long* cu_q, const long long* cu_k, const void* q,
+                                 const void* k, const void* v, const void* o, const float* lse,
+                                 const void* dO, void* dq, void* dk, void* dv, void* ws,
+                                 size_t ws_bytes, void* stream);
+
+/*
  * Paged key/value cache of 8-bit values for an attention layer's decoding.
  * A page holds `page` tokens (16, 32, 64 or 128) of all Hk key heads:
  *

@@ -41,9 +41,10 @@ def visible(lq, lk, causal, window):
 
 def attention(q, k, v, causal=True, window=0, scale=None, do=None):
     """One sequence: q [Tq, Hq, d], k, v [Tk, Hk, d].  Returns a dict with ``o``, ``lse``
-    and, with ``do``, ``dq, dk, dv``; and for each ``<name>_abs``, the sum of the absolute
-    terms whose weights a kernel rounds, ``dd_abs`` = sum |do||o| (what a rounded o puts
-    into do.o) with its way into dq and dk."""
+    and, with ``do``, ``dq, dk, dv``; for each ``<name>_abs``, the sum of the absolute terms
+    whose weights a kernel rounds; and what errors relative to sum |do||o|, to
+    sum |do| (p |v|) and to sum |do||v| in the weights' gradients come to in dq and dk
+    (``_dd``, ``_da``, ``_dp``)."""
     q, k, v = (np.asarray(t, np.float64) for t in (q, k, v))
     Tq, Hq, d = q.shape
     Tk, Hk, _ = k.shape
@@ -55,7 +56,8 @@ def attention(q, k, v, causal=True, window=0, scale=None, do=None):
         do = np.asarray(do, np.float64)
         for n, like in (("dq", q), ("dk", k), ("dv", v)):
             r[n], r[n + "_abs"] = np.zeros_like(like), np.zeros_like(like)
-        r["dq_dd"], r["dk_dd"] = np.zeros_like(q), np.zeros_like(k)
+        for n in ("_dd", "_da", "_dp"):
+            r["dq" + n], r["dk" + n] = np.zeros_like(q), np.zeros_like(k)
     if Tq == 0 or Tk == 0:
         return r
     for h in range(Hq):
@@ -79,9 +81,12 @@ def attention(q, k, v, causal=True, window=0, scale=None, do=None):
             r["dk"][:, h // G] += ds.T @ q[:, h]
             r["dq_abs"][:, h] = np.abs(ds) @ np.abs(k[:, h // G])
             r["dk_abs"][:, h // G] += np.abs(ds).T @ np.abs(q[:, h])
-            w = p * scale * (np.abs(g) * np.abs(r["o"][:, h])).sum(1, keepdims=True)
-            r["dq_dd"][:, h] = w @ np.abs(k[:, h // G])
-            r["dk_dd"][:, h // G] += w.T @ np.abs(q[:, h])
+            for n, size in (("_dd", (np.abs(g) * np.abs(r["o"][:, h])).sum(1, keepdims=True)),
+                            ("_da", (np.abs(g) * r["o_abs"][:, h]).sum(1, keepdims=True)),
+                            ("_dp", np.abs(g) @ np.abs(v[:, h // G]).T)):
+                w = p * scale * size
+                r["dq" + n][:, h] = w @ np.abs(k[:, h // G])
+                r["dk" + n][:, h // G] += w.T @ np.abs(q[:, h])
     return r
 
 

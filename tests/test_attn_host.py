@@ -147,3 +147,57 @@ def test_frequencies(m):
     for bad in (dict(rot=63), dict(rot=64, scaling="x"), dict(rot=64, base=1.0), dict(rot=64, factor=0.0)):
         with pytest.raises(ValueError):
             m.rotary_frequencies(device="cpu", **bad)
+
+
+def attn(m, backward=False, **over):
+    s = dict(B=1, Tq=8, Tk=8, Hq=4, Hk=2, d=64, causal=1, window=0, scale=0.125, q_ld=0, k_ld=0, v_ld=0)
+    a = dict(q=FAKE, k=FAKE, v=FAKE, o=FAKE, lse=FAKE)
+    if backward:
+        a.update(dO=FAKE, dq=FAKE, dk=FAKE, dv=FAKE, ws=FAKE, ws_bytes=1 << 30)
+    for n, x in over.items():
+        (s if n in s else a)[n] = x
+    shape = m.MuirAttnShape(*s.values())
+    fn = m.lib().muir_attn_bwd if backward else m.lib().muir_attn_fwd
+    return fn(ctypes.byref(shape), *a.values(), None)
+
+
+@pytest.mark.parametrize("over,code", [
+    (dict(B=-1), INVALID), (dict(Tq=-1), INVALID), (dict(Hq=0), INVALID), (dict(Hq=3), INVALID),
+    (dict(window=-1), INVALID), (dict(scale=0.0), INVALID), (dict(scale=-1.0), INVALID),
+    (dict(scale=math.nan), INVALID), (dict(scale=math.inf), INVALID), (dict(d=96), UNSUPPORTED),
+    (dict(d=256), UNSUPPORTED), (dict(q_ld=64), INVALID), (dict(k_ld=132), INVALID), (dict(v_ld=-128), INVALID),
+    (dict(B=1 << 16, Tq=1 << 16), UNSUPPORTED), (dict(B=1 << 20, Tq=1, Hq=1 << 16, Hk=1), UNSUPPORTED),
+    (dict(q=None), INVALID), (dict(k=FAKE + 8), INVALID), (dict(v=None), INVALID), (dict(o=None), INVALID),
+    (dict(lse=None), INVALID), (dict(lse=FAKE + 2), INVALID)])
+def test_attention_refusals(m, over, code):
+    assert attn(m, **over) == code
+    assert attn(m, True, **over) == code
+
+
+@pytest.mark.parametrize("over,code", [
+    (dict(dO=None), INVALID), (dict(dq=FAKE + 4), INVALID), (dict(dk=None), INVALID), (dict(dv=None), INVALID),
+    (dict(ws=None), WORKSPACE), (dict(ws_bytes=8 * 4 * 4 - 1), WORKSPACE)])
+def test_attention_backward_refusals(m, over, code):
+    assert attn(m, True, **over) == code
+
+
+@pytest.mark.parametrize("cu,ck,over,code", [
+    ([0, 8], None, dict(B=2), INVALID), ([1, 8], None, {}, INVALID), ([0, 7], None, {}, INVALID),
+    ([0, 5, 4, 8], None, {}, INVALID), ([0, 4, 8], [0, 9, 8], {}, INVALID), ([0, 8], None, dict(Tk=9), INVALID),
+    ([0, 8], [0, 8], dict(Tk=9), INVALID), (None, None, {}, INVALID), ([0], None, dict(n=0), INVALID)])
+def test_attention_varlen_refusals(m, cu, ck, over, code):
+    s = dict(B=1, Tq=8, Tk=8, Hq=4, Hk=2, d=64, causal=1, window=0, scale=0.125, q_ld=0, k_ld=0, v_ld=0)
+    n = over.pop("n", len(cu or [0, 0]) - 1)
+    s.update(over)
+    shape = m.MuirAttnShape(*s.values())
+    arr = lambda x: None if x is None else (ctypes.c_longlong * len(x))(*x)  # noqa: E731
+    for fn, rest in ((m.lib().muir_attn_fwd_varlen, [FAKE] * 5 + [None]),
+                     (m.lib().muir_attn_bwd_varlen, [FAKE] * 10 + [1 << 30, None])):
+        assert fn(ctypes.byref(shape), n, arr(cu), arr(ck), *rest) == code
+
+
+def test_attention_workspace(m):
+    s = m.MuirAttnShape(2, 100, 50, 4, 2, 64, 1, 0, 0.125, 0, 0, 0)
+    assert m.lib().muir_attn_bwd_workspace(ctypes.byref(s)) == 2 * 100 * 4 * 4
+    s.d = 32
+    assert m.lib().muir_attn_bwd_workspace(ctypes.byref(s)) == 0
