@@ -500,35 +500,40 @@ def qk_prologue_bwd(x, dy, out=None):
 # ------------------------------------------------------------------ softmax-attention layers
 
 
+# the current stream's handle and device, without building a Stream object for each call
+_raw_stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch._C._cuda_getDevice
+
+
 def _dev_call(name, t, *args):
     """Calls ``name`` with the current stream of ``t``'s device, that device current."""
-    fn = getattr(lib(), name)
+    fn = getattr(_lib or lib(), name)
     dev = t.device.index
-    stream = torch.cuda.current_stream(dev).cuda_stream
-    if dev == torch.cuda.current_device():
-        rc = fn(*args, stream)
+    if dev == _current_device():
+        rc = fn(*args, _raw_stream(dev))
     else:
         with torch.cuda.device(dev):
-            rc = fn(*args, stream)
+            rc = fn(*args, _raw_stream(dev))
     if rc != 0:
         raise MuirError(name, rc)
 
 
 def _rows(t, name, dev=None):
-    """Address and token stride of a ``[B, T, H, d]`` tensor whose heads are dense within a
-    token and whose tokens are evenly spaced (a part of a packed projection qualifies)."""
-    B, T, H, d = t.shape
-    sb, st, sh, sd = t.stride()
+    """Address and token stride (0 = dense) of a ``[B, T, H, d]`` tensor whose heads are dense
+    within a token and whose tokens are evenly spaced (a part of a packed projection
+    qualifies)."""
     if not t.is_cuda:
         raise ValueError("libmuir takes CUDA tensors only")
     if dev is not None and t.device != dev:
         raise ValueError(f"{name} is on {t.device}, not on {dev}")
+    if t.is_contiguous():
+        return t.data_ptr(), 0
+    B, T, H, d = t.shape
+    sb, st, sh, sd = t.stride()
     if (sd != 1 and d > 1) or (sh != d and H > 1):
         raise ValueError(f"{name}: channels and heads of a token must be dense")
-    if T == 1 and B > 1:
-        st = sb
-    elif T <= 1 or B * T == 0:
-        st = H * d
+    if T == 1:
+        st = sb if B > 1 else H * d
     elif B > 1 and sb != T * st:
         raise ValueError(f"{name}: tokens must be evenly spaced")
     return t.data_ptr(), st
@@ -538,7 +543,7 @@ def _same(t, name, shape, dtype, dev):
     """Address of a contiguous tensor of exactly this shape, type and device."""
     if t is None:
         return None
-    if tuple(t.shape) != tuple(shape) or t.dtype != dtype or t.device != dev or not t.is_contiguous():
+    if t.shape != shape or t.dtype != dtype or t.device != dev or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {dev}")
     return t.data_ptr()
 
@@ -591,25 +596,29 @@ def rotary(q, k=None, positions=None, inv_freq=None, interleaved=False, mscale=1
     dt = _dt(q)
     if inv_freq is None:
         raise ValueError("inv_freq is required (rotary_frequencies makes it)")
-    if q_out is None:
-        q_out = torch.empty(B, T, Hq, d, dtype=q.dtype, device=dev)
     qp, ql = _rows(q, "q")
-    op, ol = _rows(q_out, "q_out", dev)
+    if q_out is None:
+        q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
+        op, ol = q_out.data_ptr(), 0
+    else:
+        if q_out.shape != q.shape or q_out.dtype != q.dtype:
+            raise ValueError("q_out must have q's shape and dtype")
+        op, ol = _rows(q_out, "q_out", dev)
     Hk, kp, kl, kop, kol = 0, None, 0, None, 0
     if k is not None:
         if k.shape[:2] != q.shape[:2] or k.shape[3] != d or k.dtype != q.dtype:
             raise ValueError("k must have q's batch, tokens, channels and dtype")
         Hk = k.shape[2]
-        if k_out is None:
-            k_out = torch.empty(B, T, Hk, d, dtype=k.dtype, device=dev)
         kp, kl = _rows(k, "k", dev)
-        kop, kol = _rows(k_out, "k_out", dev)
-        if k_out.shape != k.shape or k_out.dtype != k.dtype:
-            raise ValueError("k_out must have k's shape and dtype")
+        if k_out is None:
+            k_out = torch.empty_like(k, memory_format=torch.contiguous_format)
+            kop, kol = k_out.data_ptr(), 0
+        else:
+            if k_out.shape != k.shape or k_out.dtype != k.dtype:
+                raise ValueError("k_out must have k's shape and dtype")
+            kop, kol = _rows(k_out, "k_out", dev)
     elif k_out is not None:
         raise ValueError("k_out without k")
-    if q_out.shape != q.shape or q_out.dtype != q.dtype:
-        raise ValueError("q_out must have q's shape and dtype")
     rot = 2 * inv_freq.numel()
     _dev_call("muir_rotary", q, B, T, Hq, Hk, d, rot, dt, qp, ql, kp, kl,
               _same(positions, "positions", (B, T), torch.int32, dev),
@@ -709,8 +718,8 @@ def kv_cache(num_pages, Hk, page, d, device="cuda"):
 
 
 def _cache(k_pages, v_pages, k_scale, v_scale, page_table, B, dev):
-    num, Hk, page, d = k_pages.shape
-    shape = (num, Hk, page, d)
+    shape = k_pages.shape
+    num, Hk, page, d = shape
     if page_table.dim() != 2 or page_table.shape[0] != B:
         raise ValueError("page_table must be [B, max_pages]")
     return MuirKvCache(
@@ -719,7 +728,7 @@ def _cache(k_pages, v_pages, k_scale, v_scale, page_table, B, dev):
         _same(v_pages, "v_pages", shape, torch.float8_e4m3fn, dev),
         _same(k_scale, "k_scale", (num, Hk), torch.float32, dev),
         _same(v_scale, "v_scale", (num, Hk), torch.float32, dev),
-        _same(page_table, "page_table", (B, page_table.shape[1]), torch.int32, dev))
+        _same(page_table, "page_table", page_table.shape, torch.int32, dev))
 
 
 def kv_append(k, v, k_pages, v_pages, k_scale, v_scale, page_table, start, count=None):
@@ -732,7 +741,7 @@ def kv_append(k, v, k_pages, v_pages, k_scale, v_scale, page_table, start, count
     dt = _dt(k)
     if v.shape != k.shape or v.dtype != k.dtype:
         raise ValueError("v must have k's shape and dtype")
-    if tuple(k_pages.shape[i] for i in (1, 3)) != (Hk, d):
+    if k_pages.shape[1] != Hk or k_pages.shape[3] != d:
         raise ValueError("the cache's heads and channels must be k's")
     c = _cache(k_pages, v_pages, k_scale, v_scale, page_table, B, dev)
     kp, kl = _rows(k, "k")
@@ -758,7 +767,7 @@ def attn_step(q, k_pages, v_pages, k_scale, v_scale, page_table, lens, scale=Non
     if o is None:
         o = torch.empty_like(q)
     op = _same(o, "o", (B, Hq, d), torch.bfloat16, dev)
-    need = lib().muir_attn_step_workspace(B, Hq, ctypes.byref(c))
+    need = (_lib or lib()).muir_attn_step_workspace(B, Hq, ctypes.byref(c))
     wsb = _workspace(need, dev, ws)
     _dev_call("muir_attn_step", q, B, Hq, ctypes.byref(c), qp,
               _same(lens, "lens", (B,), torch.int32, dev), d ** -0.5 if scale is None else scale,

@@ -594,9 +594,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_dq(const __grid_constant__
 
 template <int D>
 cudaError_t run(const Problem& p, BwdParams& a, const void* o, const void* dO, float* delta, cudaStream_t st) {
-    cudaError_t err = cudaFuncSetAttribute(k_attn_dkv<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, BwdSmem<D>::kBytes);
-    if (err == cudaSuccess)
-        err = cudaFuncSetAttribute(k_attn_dq<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, BwdSmem<D>::kBytes);
+    static std::atomic<uint64_t> done_kv{0}, done_q{0};
+    cudaError_t err = allow_smem(k_attn_dkv<D>, BwdSmem<D>::kBytes, done_kv);
+    if (err == cudaSuccess) err = allow_smem(k_attn_dq<D>, BwdSmem<D>::kBytes, done_q);
     if (err != cudaSuccess) return err;
     if (p.q_rows > 0) {
         const long long rows = p.q_rows * p.Hq;

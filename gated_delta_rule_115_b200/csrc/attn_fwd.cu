@@ -353,8 +353,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fwd(const __grid_constant_
 
 template <int D>
 cudaError_t launch(const FwdParams& a, unsigned blocks, cudaStream_t st) {
-    const cudaError_t err = cudaFuncSetAttribute(k_attn_fwd<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                 FwdSmem<D>::kBytes);
+    static std::atomic<uint64_t> done{0};
+    const cudaError_t err = allow_smem(k_attn_fwd<D>, FwdSmem<D>::kBytes, done);
     if (err != cudaSuccess) return err;
     MUIR_TIMED("k_attn_fwd", st, k_attn_fwd<D><<<blocks, kThreads, FwdSmem<D>::kBytes, st>>>(a));
     return cudaGetLastError();

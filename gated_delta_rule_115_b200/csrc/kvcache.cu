@@ -595,11 +595,13 @@ cudaError_t launch_attn_step(StepArgs a, int B, int d, void* ws, cudaStream_t st
     const int gt = (a.Hq / a.Hk + kRows - 1) / kRows;
     const dim3 grid(a.splits, a.Hk * gt, B);
     if (d == 128) {
-        err = cudaFuncSetAttribute(k_attn_step<128>, cudaFuncAttributeMaxDynamicSharedMemorySize, StepSmem<128>::kBytes);
+        static std::atomic<uint64_t> done{0};
+        err = allow_smem(k_attn_step<128>, StepSmem<128>::kBytes, done);
         if (err != cudaSuccess) return err;
         MUIR_TIMED("k_attn_step", st, k_attn_step<128><<<grid, kStepThreads, StepSmem<128>::kBytes, st>>>(a));
     } else {
-        err = cudaFuncSetAttribute(k_attn_step<64>, cudaFuncAttributeMaxDynamicSharedMemorySize, StepSmem<64>::kBytes);
+        static std::atomic<uint64_t> done{0};
+        err = allow_smem(k_attn_step<64>, StepSmem<64>::kBytes, done);
         if (err != cudaSuccess) return err;
         MUIR_TIMED("k_attn_step", st, k_attn_step<64><<<grid, kStepThreads, StepSmem<64>::kBytes, st>>>(a));
     }

@@ -5,6 +5,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 namespace muir {
 
 // Token-major 16-bit tensor [tokens][heads][d] whose tokens lie `ld` elements apart:
@@ -17,5 +19,19 @@ cudaError_t make_tmap_tokens(CUtensorMap* m, const void* base, int d, int heads,
 // codes, swizzled over the row's d bytes (64 or 128).  Coordinates (channel, row, block).
 cudaError_t make_tmap_u8(CUtensorMap* m, const void* base, int d, int page, uint64_t blocks,
                          int box_rows);
+
+// Allows kernel `f` `bytes` of dynamic shared memory on the current device, once for each
+// device (`done`: the caller's static, one bit a device; devices past 63 are set every time).
+template <class F>
+cudaError_t allow_smem(F* f, int bytes, std::atomic<uint64_t>& done) {
+    int dev = 0;
+    cudaError_t err = cudaGetDevice(&dev);
+    if (err != cudaSuccess) return err;
+    const uint64_t bit = dev < 64 ? (uint64_t)1 << dev : 0;
+    if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+    err = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (err == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+    return err;
+}
 
 }  // namespace muir
