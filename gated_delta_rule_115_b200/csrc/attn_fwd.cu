@@ -7,13 +7,14 @@
 // One block takes two tiles of 128 queries of one head of one sequence and walks the keys in
 // tiles of 128 once, with the running maximum and sum of each row (base 2, float32).  The
 // score product lands in tensor memory, four warps a tile turn it into weights -- a row to a
-// thread, so that no row is reduced across threads -- and write them back over the scores as
-// the A operand of the second product, whose sum stays in tensor memory until the end.  The
-// two tiles run half a step apart: while the threads of one work on its exponentials, the
-// tensor cores run the products of the other.
+// thread, so that no row is reduced across threads -- and write them beside the scores as
+// the A operand of the second product, whose sum stays in tensor memory until the end.  A
+// step's scores leave their place for registers at once, so the next ones (of the other tile,
+// or of the next step) are formed while these are still at their exponentials, and no thread
+// waits for a product that it does not need yet.
 //
-//   warps 0-3, 4-7 : softmax of tile 0, 1     warp 8 : issues every product
-//   warp 9         : loads (TMA, a ring of key and value tiles)
+//   warps 0-3, 4-7 : softmax of tile 0, 1     warps 8, 9 : issue the two products
+//   warp 10        : loads (TMA, a ring of key and value tiles)
 //
 // The maximum that the weights are taken against moves only when a row outgrows it by 2^8:
 // weights up to 2^8 lose nothing in bf16, and the sum in tensor memory is rescaled a few
@@ -35,7 +36,7 @@ __device__ unsigned int g_fwd_timeouts;
 
 namespace {
 
-constexpr int kThreads = 320;
+constexpr int kThreads = 352;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kSlack = 8.f;  // log2 of how far a weight may exceed 1
@@ -66,7 +67,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fwd(const __grid_constant_
     extern __shared__ __align__(1024) unsigned char sm[];
     uint64_t* q_full = reinterpret_cast<uint64_t*>(sm + SM::kBars);
     uint64_t* s_full = q_full + 2;     // scores of a tile's step are in tensor memory
-    uint64_t* p_full = s_full + 2;     // its weights are
+    uint64_t* s_free = s_full + 2;     // a place for scores has been read (one place: only the first)
+    uint64_t* p_full = s_free + 2;     // a tile's weights are in tensor memory
     uint64_t* pv_done = p_full + 2;    // its second product has finished
     uint64_t* kv_full = pv_done + 2;
     uint64_t* kv_empty = kv_full + NS;
@@ -103,6 +105,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fwd(const __grid_constant_
         for (int i = 0; i < 2; ++i) {
             mbar_init(q_full + i, 1);
             mbar_init(s_full + i, 1);
+            mbar_init(s_free + i, 4);
             mbar_init(p_full + i, 4);
             mbar_init(pv_done + i, 1);
         }
@@ -118,10 +121,14 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fwd(const __grid_constant_
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    const uint32_t tS[2] = {tmem, tmem + 128u}, tO[2] = {tmem + 256u, tmem + 256u + (uint32_t)D};
+    // columns: scores (one place for both tiles at D = 128, else one each), weights, sums
+    constexpr int SLOTS = D == 128 ? 1 : 2;
+    const uint32_t tS[2] = {tmem, tmem + (SLOTS - 1) * 128u};
+    const uint32_t tP[2] = {tmem + SLOTS * 128u, tmem + SLOTS * 128u + 64u};
+    const uint32_t tO[2] = {tmem + SLOTS * 128u + 128u, tmem + SLOTS * 128u + 128u + (uint32_t)D};
     bool bad = false;
 
-    if (warp == 9) {
+    if (warp == 10) {
         // ---------------------------------------------------------------- loads
         if (lane == 0) {
             for (int t = 0; t < 2; ++t)
@@ -162,61 +169,64 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fwd(const __grid_constant_
         }
         if (bad && lane == 0) atomicOr(&g_fwd_timeouts, 1u);
     } else if (warp == 8) {
-        // ---------------------------------------------------------------- products
-        if (lane == 0 && loads > 0) {
+        // ---------------------------------------------------------------- scores
+        // Step j of tile 0, of tile 1, step j + 1 of tile 0, ...: the order in which the
+        // tiles, half a step apart, come to need them.
+        if (lane == 0) {
             constexpr uint32_t id_s = idesc(kBF16, 128, 128, false, false);
-            constexpr uint32_t id_o = idesc(kBF16, 128, D, false, true);
-            int ns[2] = {lo[0], lo[1]};  // next score product of each tile
-            int np[2] = {lo[0], lo[1]};  // next output product
-            uint64_t t0 = globaltimer();
-            int idle = 0;
-            while (np[0] < hi[0] || np[1] < hi[1]) {
-                bool moved = false;
+            int n = 0;  // score products issued
+            for (int j = jlo; j < jhi && !bad; ++j) {
+                const int i = 2 * (j - jlo), st = i % NS;
+                const uint32_t b = saddr(sm + SM::kRing + st * SM::kTileBytes);
 #pragma unroll
                 for (int t = 0; t < 2; ++t) {
-                    if (ns[t] < hi[t] && ns[t] == np[t]) {
-                        // the scores' place is free once the weights there have been used
-                        const int j = ns[t], i = 2 * (j - jlo), st = i % NS;
-                        if ((j == lo[t] ? mbar_test(q_full + t, 0) : mbar_test(pv_done + t, (j - 1 - lo[t]) & 1)) &&
-                            mbar_test(kv_full + st, (i / NS) & 1)) {
-                            tc_fence_after();
-                            const uint32_t a = saddr(sm + t * SM::kTileBytes);
-                            const uint32_t b = saddr(sm + SM::kRing + st * SM::kTileBytes);
-#pragma unroll
-                            for (int k = 0; k < D; k += 16)
-                                mma_f16(tS[t], kdesc16(a, 0, k), kdesc16(b, 0, k), id_s, k ? 1u : 0u);
-                            mma_commit(s_full + t);
-                            ns[t] = j + 1;
-                            const int u = 1 - t;
-                            if ((j < lo[u] || j >= hi[u] || ns[u] > j) && i + NS < loads) mma_commit(kv_empty + st);
-                            moved = true;
-                        }
-                    } else if (ns[t] > np[t]) {
-                        const int j = np[t], i = 2 * (j - jlo) + 1, st = i % NS;
-                        if (mbar_test(p_full + t, (j - lo[t]) & 1) && mbar_test(kv_full + st, (i / NS) & 1)) {
-                            tc_fence_after();
-                            const uint32_t b = saddr(sm + SM::kRing + st * SM::kTileBytes);
-#pragma unroll
-                            for (int k = 0; k < kTile; k += 16)
-                                mma_f16_ta(tO[t], tS[t] + k / 2, mdesc16(b, k, 0), id_o, (j > lo[t] || k) ? 1u : 0u);
-                            mma_commit(pv_done + t);
-                            np[t] = j + 1;
-                            const int u = 1 - t;
-                            if ((j < lo[u] || j >= hi[u] || np[u] > j) && i + NS < loads) mma_commit(kv_empty + st);
-                            moved = true;
-                        }
-                    }
-                }
-                if (moved) {
-                    idle = 0;
-                } else if ((++idle & 1023) == 0) {
-                    if (idle == 1024) t0 = globaltimer();
-                    else if (globaltimer() - t0 > kWaitNs) {
-                        atomicOr(&g_fwd_timeouts, 2u);
+                    if (j < lo[t] || j >= hi[t]) continue;
+                    bool ok = mbar_wait(kv_full + st, (i / NS) & 1);
+                    if (j == lo[t]) ok = ok && mbar_wait(q_full + t, 0);
+                    // the place is free once the scores before have been read from it
+                    if (SLOTS == 1) ok = ok && (n == 0 || mbar_wait(s_free, (n - 1) & 1));
+                    else ok = ok && (j == lo[t] || mbar_wait(s_free + t, (j - 1 - lo[t]) & 1));
+                    if (!ok) {
+                        bad = true;
                         break;
                     }
+                    ++n;
+                    tc_fence_after();
+                    const uint32_t a = saddr(sm + t * SM::kTileBytes);
+#pragma unroll
+                    for (int k = 0; k < D; k += 16)
+                        mma_f16(tS[t], kdesc16(a, 0, k), kdesc16(b, 0, k), id_s, k ? 1u : 0u);
+                    mma_commit(s_full + t);
+                    // the last tile that needs these keys gives their place back
+                    if ((t == 1 || j < lo[1] || j >= hi[1]) && i + NS < loads) mma_commit(kv_empty + st);
                 }
             }
+            if (bad) atomicOr(&g_fwd_timeouts, 2u);
+        }
+    } else if (warp == 9) {
+        // ---------------------------------------------------------------- weights times values
+        // A warp of its own: the tensor cores have work while either warp waits for its next.
+        if (lane == 0) {
+            constexpr uint32_t id_o = idesc(kBF16, 128, D, false, true);
+            for (int j = jlo; j < jhi && !bad; ++j) {
+                const int i = 2 * (j - jlo) + 1, st = i % NS;
+                const uint32_t b = saddr(sm + SM::kRing + st * SM::kTileBytes);
+#pragma unroll
+                for (int t = 0; t < 2; ++t) {
+                    if (j < lo[t] || j >= hi[t]) continue;
+                    if (!mbar_wait(kv_full + st, (i / NS) & 1) || !mbar_wait(p_full + t, (j - lo[t]) & 1)) {
+                        bad = true;
+                        break;
+                    }
+                    tc_fence_after();
+#pragma unroll
+                    for (int k = 0; k < kTile; k += 16)
+                        mma_f16_ta(tO[t], tP[t] + k / 2, mdesc16(b, k, 0), id_o, (j > lo[t] || k) ? 1u : 0u);
+                    if ((t == 1 || j < lo[1] || j >= hi[1]) && i + NS < loads) mma_commit(kv_empty + st);
+                    mma_commit(pv_done + t);
+                }
+            }
+            if (bad) atomicOr(&g_fwd_timeouts, 8u);
         }
     } else {
         // ---------------------------------------------------------------- softmax
@@ -244,6 +254,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fwd(const __grid_constant_
 #pragma unroll
             for (int i = 0; i < 4; ++i) tmem_ld32(tS[t] + lane0 + 32 * i, s[i]);
             tmem_wait_ld();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(s_free + (SLOTS == 1 ? 0 : t));
             const int k0 = j * kTile;
             if (k0 + kTile - 1 > all_max || k0 < all_min) {
                 const int a = kmin - k0, b = kmax - k0;
@@ -264,6 +277,15 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fwd(const __grid_constant_
             // the callers' scale is required to be positive
             const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
             const bool grow = top > m + kSlack || (m == -INFINITY && top > -INFINITY);
+            // the sums and the weights' place are the threads' once the step before is done
+            if (j > lo[t]) {
+                const bool done = mbar_wait(pv_done + t, (j - 1 - lo[t]) & 1);
+                if (!__all_sync(0xffffffffu, done)) {
+                    bad = true;
+                    break;
+                }
+                tc_fence_after();
+            }
             if (__any_sync(0xffffffffu, grow)) {
                 const float mn = fmaxf(m, top);
                 const float a = mn == -INFINITY ? 1.f : ex2(m - mn);
@@ -294,7 +316,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fwd(const __grid_constant_
                     sum[2 + (x & 1)] += e1;
                     w[x] = bf16x2(e0, e1);
                 }
-                tmem_st32u(tS[t] + lane0 + 32 * i, w);
+                tmem_st32u(tP[t] + lane0 + 32 * i, w);
             }
             l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
             tmem_wait_st();
