@@ -17,8 +17,10 @@
 // the pair into ds, and write them, rounded to bf16 (half a step, 2^-8), over the columns of S
 // that they have read, where they are the A operand of the products that follow.
 //
-//   warps 0-3, 4-7 : p and ds of columns 0-63, 64-127     warp 8 : issues every product
-//   warp 9         : loads (TMA)
+//   warps 0-3, 4-7 : p and ds of columns 0-63, 64-127
+//   warps 8, 9, 10 : issue S, P, and the sums' products; a warp each, so that the tensor
+//                    cores have work while one waits for its next operands
+//   warp 11        : loads (TMA)
 //
 // Bound by the tensor cores (14 d flops a visible pair here) with the exponentials close
 // behind (2 a pair, 16 a clock and SM).
@@ -33,7 +35,7 @@ __device__ unsigned int g_bwd_timeouts;
 
 namespace {
 
-constexpr int kThreads = 320;
+constexpr int kThreads = 384;
 constexpr float kLog2e = 1.4426950408889634f;
 
 struct BwdParams {
@@ -84,47 +86,14 @@ __global__ void __launch_bounds__(256) k_attn_delta(const __nv_bfloat16* __restr
 // ------------------------------------------------------------------ dk, dv
 
 template <int D>
-struct BwdSmem {
+struct DkvSmem {
     static constexpr int kTileBytes = kTile * D * 2;
-    static constexpr int kStages = D == 128 ? 2 : 4;
+    static constexpr int kStages = D == 128 ? 2 : 4;                   // pairs of query and dO tiles
     static constexpr int kRing = 2 * kTileBytes;                       // after the two resident tiles
     static constexpr int kVec = kRing + kStages * 2 * kTileBytes;      // -lse log2 e and D of a stage's rows
     static constexpr int kBars = kVec + kStages * 2 * kTile * 4;
     static constexpr int kBytes = kBars + 256;
 };
-
-// A block's barriers.
-template <int NS>
-struct Bars {
-    uint64_t res_full;     // the resident tiles
-    uint64_t s_full[2];    // scores (of even, odd steps)
-    uint64_t dp_full;      // dO . v
-    uint64_t p_full;       // p written (8 warps)
-    uint64_t ds_full;      // ds written (8 warps)
-    uint64_t acc_done;     // a step's last product
-    uint64_t final_done;   // the last step's
-    uint64_t full[NS], empty[NS];
-    uint64_t tail_bar;
-    uint32_t tmem_slot;
-};
-
-template <int NS>
-__device__ __forceinline__ void init_bars(Bars<NS>* b) {
-    mbar_init(&b->res_full, 1);
-    mbar_init(b->s_full, 1);
-    mbar_init(b->s_full + 1, 1);
-    mbar_init(&b->dp_full, 1);
-    mbar_init(&b->p_full, 8);
-    mbar_init(&b->ds_full, 8);
-    mbar_init(&b->acc_done, 1);
-    mbar_init(&b->final_done, 1);
-    for (int i = 0; i < NS; ++i) {
-        mbar_init(b->full + i, 2);
-        mbar_init(b->empty + i, 1);
-    }
-    mbar_init(&b->tail_bar, 1);
-    fence_barrier_init();
-}
 
 // Whole-warp bounded wait.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity) {
@@ -191,17 +160,28 @@ __device__ __forceinline__ void store_rows(uint32_t tsrc, float f, bool any, uns
     }
 }
 
+template <int NS>
+struct DkvBars {
+    uint64_t res_full;                 // the resident tiles
+    uint64_t full[NS], empty[NS], tail;
+    uint64_t s_full[2], dp_full;       // products of a step in tensor memory (S of even, odd steps)
+    uint64_t p_full[2], dp_read, ds_full;  // eight warps: p written, P read, ds written
+    uint64_t acc_done, final_done;     // a step's last product, the last step's
+    uint32_t tmem_slot;
+};
+
 // dk and dv of 128 keys of one key head: rows of the products are keys, columns queries.
 //
 // S of a step sits in one half of 256 columns, P in the other; p and ds overwrite S, and the
-// next step's S goes to where P was, as soon as ds is formed -- so that the exponentials of
-// the next step run beside this step's last products.
+// next step's S goes to where P was, as soon as P has been read -- so that the exponentials
+// of the next step run beside this step's last products.
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1) k_attn_dkv(const __grid_constant__ BwdParams p) {
-    using SM = BwdSmem<D>;
+    using SM = DkvSmem<D>;
     constexpr int NS = SM::kStages;
     extern __shared__ __align__(1024) unsigned char sm[];
-    Bars<NS>* bar = reinterpret_cast<Bars<NS>*>(sm + SM::kBars);
+    DkvBars<NS>* bar = reinterpret_cast<DkvBars<NS>*>(sm + SM::kBars);
+    static_assert(sizeof(DkvBars<NS>) <= SM::kBytes - SM::kBars, "barriers");
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int blk = blockIdx.x / p.Hk, hk = blockIdx.x % p.Hk;
@@ -220,7 +200,24 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_dkv(const __grid_constant_
     }
     const int per = max(0, hi - lo), steps = per * G;
 
-    if (threadIdx.x == 0) init_bars(bar);
+    if (threadIdx.x == 0) {
+        mbar_init(&bar->res_full, 1);
+        for (int i = 0; i < NS; ++i) {
+            mbar_init(bar->full + i, 2);
+            mbar_init(bar->empty + i, 1);
+        }
+        mbar_init(&bar->tail, 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(bar->s_full + i, 1);
+            mbar_init(bar->p_full + i, 8);
+        }
+        mbar_init(&bar->dp_full, 1);
+        mbar_init(&bar->dp_read, 8);
+        mbar_init(&bar->ds_full, 8);
+        mbar_init(&bar->acc_done, 1);
+        mbar_init(&bar->final_done, 1);
+        fence_barrier_init();
+    }
     if (warp == 8) tmem_alloc(&bar->tmem_slot, 512);
     tc_fence_before();
     __syncthreads();
@@ -229,7 +226,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_dkv(const __grid_constant_
     const uint32_t tV = tmem + 256u, tK = tmem + 256u + (uint32_t)D;
     float* vec = reinterpret_cast<float*>(sm + SM::kVec);
 
-    if (warp == 9) {
+    if (warp == 11) {
         // ---------------------------------------------------------------- loads
         bool ok = true;
         uint32_t tails = 0;
@@ -243,7 +240,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_dkv(const __grid_constant_
             if (i >= NS) ok = warp_wait(bar->empty + st, (i / NS - 1) & 1);
             if (!ok) break;
             ok = load_pair<D>(sm + SM::kRing + st * 2 * SM::kTileBytes, &p.tq, &p.tdo, h, sq.q0 + i0, sq.lq - i0,
-                              bar->full + st, &bar->tail_bar, tails);
+                              bar->full + st, &bar->tail, tails);
             // -lse log2 e and D of the tile's queries; -infinity (no weight at all) for rows
             // that do not exist and for queries that see no key
             float* v = vec + st * 2 * kTile;
@@ -263,65 +260,60 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_dkv(const __grid_constant_
             if (lane == 0) mbar_arrive(bar->full + st);
         }
         if (!ok && lane == 0) atomicOr(&g_bwd_timeouts, 1u);
-    } else if (warp == 8) {
+    } else if (warp >= 8) {
         // ---------------------------------------------------------------- products
-        if (lane == 0 && steps > 0) {
-            constexpr uint32_t id_s = idesc(kBF16, 128, 128, false, false);
-            constexpr uint32_t id_a = idesc(kBF16, 128, D, false, true);
-            const uint32_t ka = saddr(sm), va = saddr(sm + SM::kTileBytes);
-            auto q_of = [&](int j) { return saddr(sm + SM::kRing + (j % NS) * 2 * SM::kTileBytes); };
-            auto scores = [&](int j) {  // S of step j: K Q^T
-                const uint32_t b = q_of(j), d = tmem + (uint32_t)(j & 1) * 128u;
+        constexpr uint32_t id_s = idesc(kBF16, 128, 128, false, false);
+        constexpr uint32_t id_a = idesc(kBF16, 128, D, false, true);
+        bool ok = true;
+        if (lane != 0 || steps == 0) {
+        } else if (warp == 8) {  // S = K Q^T
+            ok = mbar_wait(&bar->res_full, 0);
+            const uint32_t a = saddr(sm);
+            for (int j = 0; j < steps && ok; ++j) {
+                ok = mbar_wait(bar->full + j % NS, (j / NS) & 1) && (j == 0 || mbar_wait(&bar->dp_read, (j - 1) & 1));
+                if (!ok) break;
+                tc_fence_after();
+                const uint32_t b = saddr(sm + SM::kRing + (j % NS) * 2 * SM::kTileBytes);
+                const uint32_t d = tmem + (uint32_t)(j & 1) * 128u;
 #pragma unroll
-                for (int k = 0; k < D; k += 16) mma_f16(d, kdesc16(ka, 0, k), kdesc16(b, 0, k), id_s, k ? 1u : 0u);
+                for (int k = 0; k < D; k += 16) mma_f16(d, kdesc16(a, 0, k), kdesc16(b, 0, k), id_s, k ? 1u : 0u);
                 mma_commit(bar->s_full + (j & 1));
-            };
-            auto dots = [&](int j) {  // P of step j: V dO^T
-                const uint32_t b = q_of(j) + SM::kTileBytes, d = tmem + (uint32_t)(1 - (j & 1)) * 128u;
-#pragma unroll
-                for (int k = 0; k < D; k += 16) mma_f16(d, kdesc16(va, 0, k), kdesc16(b, 0, k), id_s, k ? 1u : 0u);
-                mma_commit(&bar->dp_full);
-            };
-            bool ok = mbar_wait(&bar->res_full, 0) && mbar_wait(bar->full, 0);
-            tc_fence_after();
-            if (ok) {
-                scores(0);
-                dots(0);
             }
+        } else if (warp == 9) {  // P = V dO^T, where the step before kept p and ds
+            ok = mbar_wait(&bar->res_full, 0);
+            const uint32_t a = saddr(sm + SM::kTileBytes);
+            for (int j = 0; j < steps && ok; ++j) {
+                ok = mbar_wait(bar->full + j % NS, (j / NS) & 1) && (j == 0 || mbar_wait(&bar->acc_done, (j - 1) & 1));
+                if (!ok) break;
+                tc_fence_after();
+                const uint32_t b = saddr(sm + SM::kRing + (j % NS) * 2 * SM::kTileBytes + SM::kTileBytes);
+                const uint32_t d = tmem + (uint32_t)(1 - (j & 1)) * 128u;
+#pragma unroll
+                for (int k = 0; k < D; k += 16) mma_f16(d, kdesc16(a, 0, k), kdesc16(b, 0, k), id_s, k ? 1u : 0u);
+                mma_commit(&bar->dp_full);
+            }
+        } else {  // dv += p^T dO, dk += ds^T Q
             for (int j = 0; j < steps && ok; ++j) {
                 const uint32_t x = tmem + (uint32_t)(j & 1) * 128u;
-                const uint32_t qa = q_of(j), doa = qa + SM::kTileBytes;
-                ok = mbar_wait(&bar->p_full, j & 1);
+                const uint32_t q = saddr(sm + SM::kRing + (j % NS) * 2 * SM::kTileBytes), g = q + SM::kTileBytes;
+                ok = mbar_wait(bar->p_full + (j & 1), (j >> 1) & 1);
                 if (!ok) break;
                 tc_fence_after();
 #pragma unroll
                 for (int k = 0; k < kTile; k += 16)  // p: columns 0-31 of each half of S
-                    mma_f16_ta(tV, x + (k & 64) + (k & 63) / 2, mdesc16(doa, k, 0), id_a, (j || k) ? 1u : 0u);
+                    mma_f16_ta(tV, x + (k & 64) + (k & 63) / 2, mdesc16(g, k, 0), id_a, (j || k) ? 1u : 0u);
                 ok = mbar_wait(&bar->ds_full, j & 1);
                 if (!ok) break;
                 tc_fence_after();
-                const bool more = j + 1 < steps;
-                if (more) {
-                    ok = mbar_wait(bar->full + (j + 1) % NS, ((j + 1) / NS) & 1);
-                    if (!ok) break;
-                    tc_fence_after();
-                    scores(j + 1);
-                }
 #pragma unroll
                 for (int k = 0; k < kTile; k += 16)  // ds: columns 32-63 of each half of S
-                    mma_f16_ta(tK, x + 32 + (k & 64) + (k & 63) / 2, mdesc16(qa, k, 0), id_a, (j || k) ? 1u : 0u);
+                    mma_f16_ta(tK, x + 32 + (k & 64) + (k & 63) / 2, mdesc16(q, k, 0), id_a, (j || k) ? 1u : 0u);
+                // the step's S and P are long done: p and ds were made of them
                 if (j + NS < steps) mma_commit(bar->empty + j % NS);
-                if (more) {
-                    mma_commit(&bar->acc_done);
-                    ok = mbar_wait(&bar->acc_done, j & 1);  // before P of j + 1 overwrites p and ds
-                    if (!ok) break;
-                    dots(j + 1);
-                } else {
-                    mma_commit(&bar->final_done);
-                }
+                mma_commit(j + 1 < steps ? &bar->acc_done : &bar->final_done);
             }
-            if (!ok) atomicOr(&g_bwd_timeouts, 2u);
         }
+        if (!ok) atomicOr(&g_bwd_timeouts, 2u);
     } else {
         // ---------------------------------------------------------------- p, ds
         const int wg = warp >> 2;
@@ -370,7 +362,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_dkv(const __grid_constant_
             tmem_wait_st();
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&bar->p_full);
+            if (lane == 0) mbar_arrive(bar->p_full + (j & 1));
 
             ok = warp_wait(&bar->dp_full, j & 1);
             if (!ok) break;
@@ -380,6 +372,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_dkv(const __grid_constant_
                 float dp[32];
                 tmem_ld32(y + 32 * hlf, dp);
                 tmem_wait_ld();
+                if (hlf) {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bar->dp_read);
+                }
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     const float4 n = dl[8 * hlf + i];
@@ -420,15 +417,36 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_dkv(const __grid_constant_
     }
 }
 
+template <int D>
+struct DqSmem {
+    static constexpr int kTileBytes = kTile * D * 2;
+    static constexpr int kKeys = D == 128 ? 3 : 4, kVals = D == 128 ? 2 : 4;  // tiles of each ring
+    static constexpr int kK = 2 * kTileBytes;                          // after the two resident tiles
+    static constexpr int kV = kK + kKeys * kTileBytes;
+    static constexpr int kBars = kV + kVals * kTileBytes;
+    static constexpr int kBytes = kBars + 256;
+};
+
+template <int NK, int NV>
+struct DqBars {
+    uint64_t res_full;
+    uint64_t k_full[NK], k_empty[NK], v_full[NV], v_empty[NV], tail;
+    uint64_t s_full[2], dp_full;       // products of a step in tensor memory (S of even, odd steps)
+    uint64_t dp_read, ds_full[2];      // eight warps: P read, ds written
+    uint64_t acc_done[2], final_done;  // a step's last product, the last step's
+    uint32_t tmem_slot;
+};
+
 // dq of 128 queries of one head: rows of the products are queries, columns keys.  The scores
 // alternate between two places, so that a step's are formed while the step before is still
 // at its exponentials.
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1) k_attn_dq(const __grid_constant__ BwdParams p) {
-    using SM = BwdSmem<D>;
-    constexpr int NS = SM::kStages;
+    using SM = DqSmem<D>;
+    constexpr int NK = SM::kKeys, NV = SM::kVals;
     extern __shared__ __align__(1024) unsigned char sm[];
-    Bars<NS>* bar = reinterpret_cast<Bars<NS>*>(sm + SM::kBars);
+    DqBars<NK, NV>* bar = reinterpret_cast<DqBars<NK, NV>*>(sm + SM::kBars);
+    static_assert(sizeof(DqBars<NK, NV>) <= SM::kBytes - SM::kBars, "barriers");
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int blk = blockIdx.x / p.Hq, h = blockIdx.x % p.Hq;
@@ -445,7 +463,27 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_dq(const __grid_constant__
     const int lo = first / kTile;
     const int steps = last < first ? 0 : last / kTile + 1 - lo;
 
-    if (threadIdx.x == 0) init_bars(bar);
+    if (threadIdx.x == 0) {
+        mbar_init(&bar->res_full, 1);
+        for (int i = 0; i < NK; ++i) {
+            mbar_init(bar->k_full + i, 1);
+            mbar_init(bar->k_empty + i, 1);
+        }
+        for (int i = 0; i < NV; ++i) {
+            mbar_init(bar->v_full + i, 1);
+            mbar_init(bar->v_empty + i, 1);
+        }
+        mbar_init(&bar->tail, 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(bar->s_full + i, 1);
+            mbar_init(bar->ds_full + i, 8);
+            mbar_init(bar->acc_done + i, 1);
+        }
+        mbar_init(&bar->dp_full, 1);
+        mbar_init(&bar->dp_read, 8);
+        mbar_init(&bar->final_done, 1);
+        fence_barrier_init();
+    }
     if (warp == 8) tmem_alloc(&bar->tmem_slot, 512);
     tc_fence_before();
     __syncthreads();
@@ -453,72 +491,94 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_dq(const __grid_constant__
     const uint32_t tmem = bar->tmem_slot;
     const uint32_t tP = tmem + 256u, tQ = tmem + 384u;
 
-    if (warp == 9) {
+    if (warp == 11) {
+        // ---------------------------------------------------------------- loads
         bool ok = true;
-        uint32_t tails = 0;
         if (lane == 0 && steps > 0) {
             mbar_arrive_expect_tx(&bar->res_full, 2 * SM::kTileBytes);
             load_tile<D>(sm, &p.tq, h, sq.q0 + r0, &bar->res_full);
             load_tile<D>(sm + SM::kTileBytes, &p.tdo, h, sq.q0 + r0, &bar->res_full);
         }
         for (int i = 0; i < steps && ok; ++i) {
-            const int st = i % NS, j0 = (lo + i) * kTile;
-            if (i >= NS) ok = warp_wait(bar->empty + st, (i / NS - 1) & 1);
+            const int j0 = (lo + i) * kTile, rows = sq.lk - j0;
+            const int ks = i % NK, vs = i % NV;
+            if (i >= NK) ok = warp_wait(bar->k_empty + ks, (i / NK - 1) & 1);
             if (!ok) break;
-            ok = load_pair<D>(sm + SM::kRing + st * 2 * SM::kTileBytes, &p.tk, &p.tv, hk, sq.k0 + j0, sq.lk - j0,
-                              bar->full + st, &bar->tail_bar, tails);
-            if (lane == 0) mbar_arrive(bar->full + st);
+            // key rows behind the sequence's end: their ds is zero, which a NaN or an
+            // infinity there would survive (the value rows' dots are discarded instead)
+            unsigned char* kd = sm + SM::kK + ks * SM::kTileBytes;
+            uint64_t* kb = rows < kTile ? &bar->tail : bar->k_full + ks;
+            if (lane == 0) {
+                mbar_arrive_expect_tx(kb, SM::kTileBytes);
+                load_tile<D>(kd, &p.tk, hk, sq.k0 + j0, kb);
+            }
+            __syncwarp();
+            if (i >= NV) ok = warp_wait(bar->v_empty + vs, (i / NV - 1) & 1);
+            if (!ok) break;
+            if (lane == 0) {
+                mbar_arrive_expect_tx(bar->v_full + vs, SM::kTileBytes);
+                load_tile<D>(sm + SM::kV + vs * SM::kTileBytes, &p.tv, hk, sq.k0 + j0, bar->v_full + vs);
+            }
+            __syncwarp();
+            if (rows < kTile) {
+                ok = warp_wait(&bar->tail, 0);
+                if (!ok) break;
+                zero_rows<D>(kd, rows);
+                if (lane == 0) mbar_arrive(bar->k_full + ks);
+            }
         }
         if (!ok && lane == 0) atomicOr(&g_bwd_timeouts, 8u);
-    } else if (warp == 8) {
-        if (lane == 0 && steps > 0) {
-            constexpr uint32_t id_s = idesc(kBF16, 128, 128, false, false);
-            constexpr uint32_t id_a = idesc(kBF16, 128, D, false, true);
-            const uint32_t qa = saddr(sm), doa = saddr(sm + SM::kTileBytes);
-            auto k_of = [&](int j) { return saddr(sm + SM::kRing + (j % NS) * 2 * SM::kTileBytes); };
-            auto scores = [&](int j) {  // Q K^T
-                const uint32_t b = k_of(j), d = tmem + (uint32_t)(j & 1) * 128u;
-#pragma unroll
-                for (int k = 0; k < D; k += 16) mma_f16(d, kdesc16(qa, 0, k), kdesc16(b, 0, k), id_s, k ? 1u : 0u);
-                mma_commit(bar->s_full + (j & 1));
-            };
-            auto dots = [&](int j) {  // dO V^T
-                const uint32_t b = k_of(j) + SM::kTileBytes;
-#pragma unroll
-                for (int k = 0; k < D; k += 16) mma_f16(tP, kdesc16(doa, 0, k), kdesc16(b, 0, k), id_s, k ? 1u : 0u);
-                mma_commit(&bar->dp_full);
-            };
-            bool ok = mbar_wait(&bar->res_full, 0) && mbar_wait(bar->full, 0);
-            tc_fence_after();
-            if (ok) {
-                scores(0);
-                dots(0);
-            }
+    } else if (warp >= 8) {
+        // ---------------------------------------------------------------- products
+        constexpr uint32_t id_s = idesc(kBF16, 128, 128, false, false);
+        constexpr uint32_t id_a = idesc(kBF16, 128, D, false, true);
+        bool ok = true;
+        if (lane != 0 || steps == 0) {
+        } else if (warp == 8) {  // S = Q K^T, where the ds of two steps before was
+            ok = mbar_wait(&bar->res_full, 0);
+            const uint32_t a = saddr(sm);
             for (int j = 0; j < steps && ok; ++j) {
-                const bool more = j + 1 < steps;
-                if (more) {
-                    ok = mbar_wait(bar->full + (j + 1) % NS, ((j + 1) / NS) & 1);
-                    // the scores' other place is free once step j - 1's ds there has been used
-                    if (ok && j > 0) ok = mbar_wait(&bar->acc_done, (j - 1) & 1);
-                    if (!ok) break;
-                    tc_fence_after();
-                    scores(j + 1);
-                }
-                ok = mbar_wait(&bar->ds_full, j & 1);
+                ok = mbar_wait(bar->k_full + j % NK, (j / NK) & 1) &&
+                     (j < 2 || mbar_wait(bar->acc_done + (j & 1), ((j - 2) >> 1) & 1));
                 if (!ok) break;
                 tc_fence_after();
-                if (more) dots(j + 1);
-                const uint32_t x = tmem + (uint32_t)(j & 1) * 128u, b = k_of(j);
+                const uint32_t b = saddr(sm + SM::kK + (j % NK) * SM::kTileBytes);
+                const uint32_t d = tmem + (uint32_t)(j & 1) * 128u;
+#pragma unroll
+                for (int k = 0; k < D; k += 16) mma_f16(d, kdesc16(a, 0, k), kdesc16(b, 0, k), id_s, k ? 1u : 0u);
+                mma_commit(bar->s_full + (j & 1));
+            }
+        } else if (warp == 9) {  // P = dO V^T
+            ok = mbar_wait(&bar->res_full, 0);
+            const uint32_t a = saddr(sm + SM::kTileBytes);
+            for (int j = 0; j < steps && ok; ++j) {
+                ok = mbar_wait(bar->v_full + j % NV, (j / NV) & 1) && (j == 0 || mbar_wait(&bar->dp_read, (j - 1) & 1));
+                if (!ok) break;
+                tc_fence_after();
+                const uint32_t b = saddr(sm + SM::kV + (j % NV) * SM::kTileBytes);
+#pragma unroll
+                for (int k = 0; k < D; k += 16) mma_f16(tP, kdesc16(a, 0, k), kdesc16(b, 0, k), id_s, k ? 1u : 0u);
+                if (j + NV < steps) mma_commit(bar->v_empty + j % NV);
+                mma_commit(&bar->dp_full);
+            }
+        } else {  // dq += ds K
+            for (int j = 0; j < steps && ok; ++j) {
+                ok = mbar_wait(bar->ds_full + (j & 1), (j >> 1) & 1);
+                if (!ok) break;
+                tc_fence_after();
+                const uint32_t x = tmem + (uint32_t)(j & 1) * 128u;
+                const uint32_t b = saddr(sm + SM::kK + (j % NK) * SM::kTileBytes);
 #pragma unroll
                 for (int k = 0; k < kTile; k += 16)  // ds: columns 0-31 of each half of S
                     mma_f16_ta(tQ, x + (k & 64) + (k & 63) / 2, mdesc16(b, k, 0), id_a, (j || k) ? 1u : 0u);
-                if (j + NS < steps) mma_commit(bar->empty + j % NS);
-                if (j + 2 < steps) mma_commit(&bar->acc_done);
-                if (!more) mma_commit(&bar->final_done);
+                if (j + NK < steps) mma_commit(bar->k_empty + j % NK);
+                if (j + 2 < steps) mma_commit(bar->acc_done + (j & 1));
+                if (j + 1 == steps) mma_commit(&bar->final_done);
             }
-            if (!ok) atomicOr(&g_bwd_timeouts, 16u);
         }
+        if (!ok) atomicOr(&g_bwd_timeouts, 16u);
     } else {
+        // ---------------------------------------------------------------- p, ds
         const int wg = warp >> 2;
         const uint32_t lane0 = (uint32_t)(warp & 3) << 21;
         const int row = r0 + (threadIdx.x & 127);
@@ -559,6 +619,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_dq(const __grid_constant__
                 float dp[32];
                 tmem_ld32(tP + lane0 + 64 * wg + 32 * hlf, dp);
                 tmem_wait_ld();
+                if (hlf) {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bar->dp_read);
+                }
 #pragma unroll
                 for (int i = 0; i < 32; ++i) s[hlf][i] *= dp[i] - dl;
                 if (mask) {
@@ -572,7 +637,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_dq(const __grid_constant__
             tmem_wait_st();
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&bar->ds_full);
+            if (lane == 0) mbar_arrive(bar->ds_full + (j & 1));
         }
         if (steps > 0 && ok) {
             ok = warp_wait(&bar->final_done, 0);
@@ -595,8 +660,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_dq(const __grid_constant__
 template <int D>
 cudaError_t run(const Problem& p, BwdParams& a, const void* o, const void* dO, float* delta, cudaStream_t st) {
     static std::atomic<uint64_t> done_kv{0}, done_q{0};
-    cudaError_t err = allow_smem(k_attn_dkv<D>, BwdSmem<D>::kBytes, done_kv);
-    if (err == cudaSuccess) err = allow_smem(k_attn_dq<D>, BwdSmem<D>::kBytes, done_q);
+    cudaError_t err = allow_smem(k_attn_dkv<D>, DkvSmem<D>::kBytes, done_kv);
+    if (err == cudaSuccess) err = allow_smem(k_attn_dq<D>, DqSmem<D>::kBytes, done_q);
     if (err != cudaSuccess) return err;
     if (p.q_rows > 0) {
         const long long rows = p.q_rows * p.Hq;
@@ -612,14 +677,14 @@ cudaError_t run(const Problem& p, BwdParams& a, const void* o, const void* dO, f
         a.n = gather_seqs(p, i, true, kTile, a.seq, &i, &blocks);
         if (a.n == 0) continue;
         MUIR_TIMED("k_attn_dkv", st,
-                   k_attn_dkv<D><<<(unsigned)(blocks * p.Hk), kThreads, BwdSmem<D>::kBytes, st>>>(a));
+                   k_attn_dkv<D><<<(unsigned)(blocks * p.Hk), kThreads, DkvSmem<D>::kBytes, st>>>(a));
         if ((err = cudaGetLastError()) != cudaSuccess) return err;
     }
     for (int i = 0; i < p.n;) {
         a.n = gather_seqs(p, i, false, kTile, a.seq, &i, &blocks);
         if (a.n == 0) continue;
         MUIR_TIMED("k_attn_dq", st,
-                   k_attn_dq<D><<<(unsigned)(blocks * p.Hq), kThreads, BwdSmem<D>::kBytes, st>>>(a));
+                   k_attn_dq<D><<<(unsigned)(blocks * p.Hq), kThreads, DqSmem<D>::kBytes, st>>>(a));
         if ((err = cudaGetLastError()) != cudaSuccess) return err;
     }
     return cudaSuccess;
