@@ -164,17 +164,22 @@ template <int NS>
 struct DkvBars {
     uint64_t res_full;                 // the resident tiles
     uint64_t full[NS], empty[NS], tail;
-    uint64_t s_full[2], dp_full;       // products of a step in tensor memory (S of even, odd steps)
-    uint64_t p_full[2], dp_read, ds_full;  // eight warps: p written, P read, ds written
-    uint64_t acc_done, final_done;     // a step's last product, the last step's
+    // of each half of the columns:
+    uint64_t s_full[2], dp_full[2];             // its products of a step in tensor memory
+    uint64_t p_full[2], dp_read[2], ds_full[2]; // four warps: p written, P read, ds written
+    uint64_t acc_done[2];                       // its last product of a step
+    uint64_t final_done;
     uint32_t tmem_slot;
 };
 
 // dk and dv of 128 keys of one key head: rows of the products are keys, columns queries.
 //
-// S of a step sits in one half of 256 columns, P in the other; p and ds overwrite S, and the
-// next step's S goes to where P was, as soon as P has been read -- so that the exponentials
-// of the next step run beside this step's last products.
+// The 128 queries of a step are two halves of 64 that go their own ways, each with its four
+// warps, its barriers and 128 columns: its S in 64 of them, its P in the other 64; p and ds
+// overwrite S, and the next step's S goes to where P was as soon as P has been read.  The
+// halves drift half a step apart, so that one's exponentials run beside the other's products
+// (as one whole of 128 columns, each step waited for its own scores and its own exponentials
+// in turn: 3400 clocks a step, of which the tensor cores ran 2550).
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1) k_attn_dkv(const __grid_constant__ BwdParams p) {
     using SM = DkvSmem<D>;
@@ -209,12 +214,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_dkv(const __grid_constant_
         mbar_init(&bar->tail, 1);
         for (int i = 0; i < 2; ++i) {
             mbar_init(bar->s_full + i, 1);
-            mbar_init(bar->p_full + i, 8);
+            mbar_init(bar->dp_full + i, 1);
+            mbar_init(bar->p_full + i, 4);
+            mbar_init(bar->dp_read + i, 4);
+            mbar_init(bar->ds_full + i, 4);
+            mbar_init(bar->acc_done + i, 1);
         }
-        mbar_init(&bar->dp_full, 1);
-        mbar_init(&bar->dp_read, 8);
-        mbar_init(&bar->ds_full, 8);
-        mbar_init(&bar->acc_done, 1);
         mbar_init(&bar->final_done, 1);
         fence_barrier_init();
     }
@@ -262,7 +267,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_dkv(const __grid_constant_
         if (!ok && lane == 0) atomicOr(&g_bwd_timeouts, 1u);
     } else if (warp >= 8) {
         // ---------------------------------------------------------------- products
-        constexpr uint32_t id_s = idesc(kBF16, 128, 128, false, false);
+        constexpr uint32_t id_s = idesc(kBF16, 128, 64, false, false);
         constexpr uint32_t id_a = idesc(kBF16, 128, D, false, true);
         bool ok = true;
         if (lane != 0 || steps == 0) {
@@ -270,47 +275,61 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_dkv(const __grid_constant_
             ok = mbar_wait(&bar->res_full, 0);
             const uint32_t a = saddr(sm);
             for (int j = 0; j < steps && ok; ++j) {
-                ok = mbar_wait(bar->full + j % NS, (j / NS) & 1) && (j == 0 || mbar_wait(&bar->dp_read, (j - 1) & 1));
-                if (!ok) break;
-                tc_fence_after();
                 const uint32_t b = saddr(sm + SM::kRing + (j % NS) * 2 * SM::kTileBytes);
-                const uint32_t d = tmem + (uint32_t)(j & 1) * 128u;
+                ok = mbar_wait(bar->full + j % NS, (j / NS) & 1);
 #pragma unroll
-                for (int k = 0; k < D; k += 16) mma_f16(d, kdesc16(a, 0, k), kdesc16(b, 0, k), id_s, k ? 1u : 0u);
-                mma_commit(bar->s_full + (j & 1));
+                for (int u = 0; u < 2; ++u) {
+                    ok = ok && (j == 0 || mbar_wait(bar->dp_read + u, (j - 1) & 1));
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint32_t d = tmem + 128u * u + (uint32_t)(j & 1) * 64u;
+#pragma unroll
+                    for (int k = 0; k < D; k += 16)
+                        mma_f16(d, kdesc16(a, 0, k), kdesc16(b, 64 * u, k), id_s, k ? 1u : 0u);
+                    mma_commit(bar->s_full + u);
+                }
             }
         } else if (warp == 9) {  // P = V dO^T, where the step before kept p and ds
             ok = mbar_wait(&bar->res_full, 0);
             const uint32_t a = saddr(sm + SM::kTileBytes);
             for (int j = 0; j < steps && ok; ++j) {
-                ok = mbar_wait(bar->full + j % NS, (j / NS) & 1) && (j == 0 || mbar_wait(&bar->acc_done, (j - 1) & 1));
-                if (!ok) break;
-                tc_fence_after();
                 const uint32_t b = saddr(sm + SM::kRing + (j % NS) * 2 * SM::kTileBytes + SM::kTileBytes);
-                const uint32_t d = tmem + (uint32_t)(1 - (j & 1)) * 128u;
+                ok = mbar_wait(bar->full + j % NS, (j / NS) & 1);
 #pragma unroll
-                for (int k = 0; k < D; k += 16) mma_f16(d, kdesc16(a, 0, k), kdesc16(b, 0, k), id_s, k ? 1u : 0u);
-                mma_commit(&bar->dp_full);
+                for (int u = 0; u < 2; ++u) {
+                    ok = ok && (j == 0 || mbar_wait(bar->acc_done + u, (j - 1) & 1));
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint32_t d = tmem + 128u * u + (uint32_t)(1 - (j & 1)) * 64u;
+#pragma unroll
+                    for (int k = 0; k < D; k += 16)
+                        mma_f16(d, kdesc16(a, 0, k), kdesc16(b, 64 * u, k), id_s, k ? 1u : 0u);
+                    mma_commit(bar->dp_full + u);
+                }
             }
         } else {  // dv += p^T dO, dk += ds^T Q
             for (int j = 0; j < steps && ok; ++j) {
-                const uint32_t x = tmem + (uint32_t)(j & 1) * 128u;
                 const uint32_t q = saddr(sm + SM::kRing + (j % NS) * 2 * SM::kTileBytes), g = q + SM::kTileBytes;
-                ok = mbar_wait(bar->p_full + (j & 1), (j >> 1) & 1);
-                if (!ok) break;
-                tc_fence_after();
 #pragma unroll
-                for (int k = 0; k < kTile; k += 16)  // p: columns 0-31 of each half of S
-                    mma_f16_ta(tV, x + (k & 64) + (k & 63) / 2, mdesc16(g, k, 0), id_a, (j || k) ? 1u : 0u);
-                ok = mbar_wait(&bar->ds_full, j & 1);
-                if (!ok) break;
-                tc_fence_after();
+                for (int u = 0; u < 2; ++u) {
+                    const uint32_t x = tmem + 128u * u + (uint32_t)(j & 1) * 64u;
+                    ok = ok && mbar_wait(bar->p_full + u, j & 1);
+                    if (!ok) break;
+                    tc_fence_after();
 #pragma unroll
-                for (int k = 0; k < kTile; k += 16)  // ds: columns 32-63 of each half of S
-                    mma_f16_ta(tK, x + 32 + (k & 64) + (k & 63) / 2, mdesc16(q, k, 0), id_a, (j || k) ? 1u : 0u);
-                // the step's S and P are long done: p and ds were made of them
-                if (j + NS < steps) mma_commit(bar->empty + j % NS);
-                mma_commit(j + 1 < steps ? &bar->acc_done : &bar->final_done);
+                    for (int k = 0; k < 64; k += 16)  // p: the first 32 columns of S
+                        mma_f16_ta(tV, x + k / 2, mdesc16(g, 64 * u + k, 0), id_a, (j || u || k) ? 1u : 0u);
+                    ok = mbar_wait(bar->ds_full + u, j & 1);
+                    if (!ok) break;
+                    tc_fence_after();
+#pragma unroll
+                    for (int k = 0; k < 64; k += 16)  // ds: the others
+                        mma_f16_ta(tK, x + 32 + k / 2, mdesc16(q, 64 * u + k, 0), id_a, (j || u || k) ? 1u : 0u);
+                    // the step's S and P are long done: p and ds were made of them
+                    if (u == 1 && j + NS < steps) mma_commit(bar->empty + j % NS);
+                    if (j + 1 < steps) mma_commit(bar->acc_done + u);
+                }
+                if (ok && j + 1 == steps) mma_commit(&bar->final_done);
             }
         }
         if (!ok) atomicOr(&g_bwd_timeouts, 2u);
@@ -322,8 +341,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_dkv(const __grid_constant_
         const float c = p.scale_log2;
         bool ok = true;
         for (int j = 0; j < steps && ok; ++j) {
-            const uint32_t x = tmem + lane0 + (uint32_t)(j & 1) * 128u + 64u * wg;
-            const uint32_t y = tmem + lane0 + (uint32_t)(1 - (j & 1)) * 128u + 64u * wg;
+            const uint32_t x = tmem + lane0 + 128u * wg + (uint32_t)(j & 1) * 64u;
+            const uint32_t y = tmem + lane0 + 128u * wg + (uint32_t)(1 - (j & 1)) * 64u;
             const float4* nl = reinterpret_cast<const float4*>(vec + (j % NS) * 2 * kTile + 64 * wg);
             const float4* dl = nl + kTile / 4;
             const int i0 = (lo + j % per) * kTile;
@@ -335,7 +354,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_dkv(const __grid_constant_
                 if (p.causal) a = first;
                 if (p.window) b = min(b, first + p.window);
             }
-            ok = warp_wait(bar->s_full + (j & 1), (j >> 1) & 1) && warp_wait(bar->full + j % NS, (j / NS) & 1);
+            ok = warp_wait(bar->s_full + wg, j & 1) && warp_wait(bar->full + j % NS, (j / NS) & 1);
             if (!ok) break;
             tc_fence_after();
             float s[2][32];
@@ -362,9 +381,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_dkv(const __grid_constant_
             tmem_wait_st();
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(bar->p_full + (j & 1));
+            if (lane == 0) mbar_arrive(bar->p_full + wg);
 
-            ok = warp_wait(&bar->dp_full, j & 1);
+            ok = warp_wait(bar->dp_full + wg, j & 1);
             if (!ok) break;
             tc_fence_after();
 #pragma unroll
@@ -375,7 +394,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_dkv(const __grid_constant_
                 if (hlf) {
                     tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(&bar->dp_read);
+                    if (lane == 0) mbar_arrive(bar->dp_read + wg);
                 }
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
@@ -397,7 +416,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_dkv(const __grid_constant_
             tmem_wait_st();
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&bar->ds_full);
+            if (lane == 0) mbar_arrive(bar->ds_full + wg);
         }
         if (steps > 0 && ok) {
             ok = warp_wait(&bar->final_done, 0);
