@@ -143,15 +143,19 @@ __global__ void __launch_bounds__(kAppThreads) k_kv_append(AppendArgs p) {
 
 // ------------------------------------------------------------------ step
 
-// Keys and values travel in stages of kStepKeys keys, copied by TMA into a swizzled
-// ring by one warp that runs ahead; four warps take 16 keys of each stage.
-constexpr int kStepKeys = 64;
-constexpr int kStepWarps = 4;              // consumer warps, 16 keys of a stage each
+// Keys and values travel in stages of kStepKeys keys, copied by TMA into a swizzled ring by
+// one warp that runs ahead; each of four warps takes 32 keys of a stage.
+constexpr int kStepKeys = 128;
+constexpr int kStepWarps = 4;
+constexpr int kWarpKeys = kStepKeys / kStepWarps;
 constexpr int kStepThreads = 32 * (kStepWarps + 1);
-constexpr int kStepStages = 4;
-constexpr int kRows = 16;                  // query rows of an MMA: the heads that share a key head
+constexpr int kStepStages = 3;
+constexpr int kGroups = kStepKeys / 16;    // groups of 16 keys, within one page each
+constexpr int kMaxRows = 16;               // query heads of a block
+constexpr float kSlack = 8.f;              // log2 of how far a weight may exceed 1
+constexpr float kWeightExp = 7.f;          // fp16 weights are 2^(score - reference + 7) <= 2^15
 
-struct StepMeta {        // per 16 keys of a stage
+struct StepMeta {        // per group of a stage
     float ks, lv;        // key scale, log2 of the value scale
     int lo, hi;          // visible keys [lo, hi) of the 16
 };
@@ -160,8 +164,9 @@ template <int D>
 struct StepSmem {
     static constexpr int kTile = kStepKeys * D;               // bytes of K (or V) in a stage
     static constexpr int kMeta = kStepStages * 2 * kTile;
-    static constexpr int kBars = kMeta + kStepStages * 4 * (int)sizeof(StepMeta);
+    static constexpr int kBars = kMeta + kStepStages * kGroups * (int)sizeof(StepMeta);
     static constexpr int kBytes = kBars + 2 * kStepStages * 8;
+    static_assert(kStepWarps * kMaxRows * (D + 2) * 4 <= kMeta, "the warps' parts reuse the ring");
 };
 
 __device__ __forceinline__ uint32_t h2_from_e4m3(uint32_t two) {
@@ -175,13 +180,20 @@ __device__ __forceinline__ uint32_t h2_from_e4m3_hi(uint32_t two) {
     return r;
 }
 
-__device__ __forceinline__ void mma_f16_16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
-                                              uint32_t b1) {
+__device__ __forceinline__ void mma_f16_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                              uint32_t b0, uint32_t b1) {
     asm volatile(
         "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
         "{%0,%1,%2,%3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// Transposes an 8 x 8 matrix of 16-bit values held one row to four lanes.
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+    uint32_t r;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+    return r;
 }
 
 __device__ __forceinline__ float ex2(float x) {
@@ -202,29 +214,33 @@ __device__ __forceinline__ uint32_t step_off(int r, int c) {
                     : (uint32_t)r * 64u + (uint32_t)((c ^ ((r >> 1) & 3)) << 4);
 }
 
-// One block: the heads of one key head (16 at a time) of one sequence over one range of
-// its keys.
+// One block: up to 8 HT query heads of one key head of one sequence over one range of its
+// keys.
 //
-// The products run on mma.sync m16n8k16 in fp16 with float32 sums: the rows are the
-// query heads that share the key head (of 16, the rest zero), so a key costs 16 rows
-// whatever the group, and the kernel stays bound by the cache's bytes.  e4m3 codes are
-// exact in fp16.  A product's contraction may run in any order as long as both operands
-// agree: lane (g, c) takes 32 (16 for d = 64) neighbouring bytes of key g for the score
-// product, and 16 (8) neighbouring columns of keys 2c, 2c+1, 2c+8, 2c+9 for the output,
-// so both read shared memory in 16-byte vectors, conflict-free, with no transposition.
+// Both products run transposed on mma.sync m16n8k16, in fp16 with float32 sums: keys (then
+// channels) are the 16 rows and query heads the 8 columns, so that the cache's side, which
+// is all the work there is, fills the instruction at any group size; with the heads as rows
+// instead, four heads left 12 of 16 rows empty and the kernel was bound by issue slots
+// (167 us for 64 streams of 16384 tokens, 4 key heads; 46% of the rate of HBM).  e4m3 codes
+// are exact in fp16.  A product's contraction may run in any order as long as both operands
+// agree: lane (g, c) takes D/4 neighbouring bytes of keys g and g + 8 for the scores, and
+// D/8 neighbouring channels of keys 2c, 2c+1, 2c+8, 2c+9 for the output, so both read shared
+// memory in 16-byte vectors without a transposition; the weights, which the score product
+// leaves by key and the output product takes by head, are transposed in registers.
 //
 // Query rows are scaled by a power of two to a largest magnitude in [2^13, 2^14): fp16
 // then holds bf16 values exactly down to 2^-28 of the row's largest.  Softmax runs in
-// base 2 with running maxima held in float32: m over the scores for the normaliser, and
-// M over score + log2(value scale) for the weights of the value codes, which are kept as
-// fp16(2^(score + log2 scale - M + 15)): relative rounding 2^-11 down to 2^-29 of the
-// largest weight whatever the pages' scales, where a weight without its page's scale
-// could vanish next to a page of large values.
-template <int D>
-__global__ void __launch_bounds__(kStepThreads) k_attn_step(const __grid_constant__ StepArgs p) {
+// base 2 against references held in float32 that move only when a score outgrows them by
+// 2^8: m over the scores for the normaliser, and M over score + log2(value scale) for the
+// weights of the value codes, which are kept as fp16(2^(score + log2 scale - M + 7)):
+// relative rounding 2^-11 down to 2^-21 of the reference whatever the pages' scales, where
+// a weight without its page's scale could vanish next to a page of large values.
+template <int D, int HT>
+__global__ void __launch_bounds__(kStepThreads, HT == 1 ? 2 : 1) k_attn_step(const __grid_constant__ StepArgs p) {
     using SM = StepSmem<D>;
     constexpr int KSTEPS = D / 16;   // 16-deep steps of the score product
-    constexpr int NT = D / 8;        // 8-column tiles of the output product
+    constexpr int NT = D / 16;       // 16-channel tiles of the output product
+    constexpr int ROWS = 8 * HT;
     extern __shared__ __align__(1024) unsigned char sm[];
     uint64_t* full = reinterpret_cast<uint64_t*>(sm + SM::kBars);
     uint64_t* empty = full + kStepStages;
@@ -232,8 +248,8 @@ __global__ void __launch_bounds__(kStepThreads) k_attn_step(const __grid_constan
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int G = p.Hq / p.Hk;
-    const int gtiles = (G + kRows - 1) / kRows;
-    const int hk = blockIdx.y / gtiles, g0 = (blockIdx.y % gtiles) * kRows;
+    const int gtiles = (G + ROWS - 1) / ROWS;
+    const int hk = blockIdx.y / gtiles, g0 = (blockIdx.y % gtiles) * ROWS;
     const int b = blockIdx.z, split = blockIdx.x;
 
     long long len = p.lens[b];
@@ -260,16 +276,14 @@ __global__ void __launch_bounds__(kStepThreads) k_attn_step(const __grid_constan
     bool bad = false;
 
     if (warp == kStepWarps) {
-        // ---- producer: page ids and scales 32 pieces ahead, one piece = min(page, 64)
-        // keys, or the 64 keys of a stage inside a longer page
-        const int piece = p.page < kStepKeys ? p.page : kStepKeys;
-        const int per_stage = kStepKeys / piece;
-        const int npiece = nst * per_stage;
-        for (int i0 = 0; i0 < npiece && !bad; i0 += 32) {
+        // ---- producer: page ids and scales 32 pages ahead, one copy a page
+        const int per_stage = kStepKeys / p.page;
+        const int npage = nst * per_stage;
+        for (int i0 = 0; i0 < npage && !bad; i0 += 32) {
             int id = -1;
             float ks = 0.f, vs = 0.f;
-            const long long key = lo + (long long)(i0 + lane) * piece;
-            if (i0 + lane < npiece && key < hi) {
+            const long long key = lo + (long long)(i0 + lane) * p.page;
+            if (i0 + lane < npage && key < hi) {
                 id = p.table[(long long)b * p.max_pages + key / p.page];
                 if (id < 0 || id >= p.num_pages) id = -1;
                 if (id >= 0) {
@@ -277,7 +291,7 @@ __global__ void __launch_bounds__(kStepThreads) k_attn_step(const __grid_constan
                     vs = p.v_scale[(long long)id * p.Hk + hk];
                 }
             }
-            const int n = min(32, npiece - i0);
+            const int n = min(32, npage - i0);
             for (int i = 0; i < n; i += per_stage) {
                 const int st = (i0 + i) / per_stage, slot = st % kStepStages;
                 if (st >= kStepStages) {
@@ -287,36 +301,30 @@ __global__ void __launch_bounds__(kStepThreads) k_attn_step(const __grid_constan
                         break;
                     }
                 }
-                unsigned char* kd = sm + (size_t)slot * 2 * SM::kTile;
-                // metadata of the stage's four groups of 16 keys
-                const int src = i + (lane * 16) / piece;
+                // metadata of the stage's groups
+                const int src = i + (lane * 16) / p.page;
                 const int gid = __shfl_sync(0xffffffffu, id, src & 31);
                 const float gks = __shfl_sync(0xffffffffu, ks, src & 31);
                 const float gvs = __shfl_sync(0xffffffffu, vs, src & 31);
-                if (lane < 4) {
+                if (lane < kGroups) {
                     const long long k0 = lo + (long long)st * kStepKeys + lane * 16;
                     StepMeta m;
                     m.ks = gks;
                     m.lv = __log2f(gvs);
                     m.lo = (int)max(0LL, min(16LL, first - k0));
                     m.hi = gid < 0 ? 0 : (int)max(0LL, min(16LL, hi - k0));
-                    meta[slot * 4 + lane] = m;
+                    meta[slot * kGroups + lane] = m;
                 }
-                int copies = 0;
-                for (int j = 0; j < per_stage; ++j)
-                    copies += __shfl_sync(0xffffffffu, id, (i + j) & 31) >= 0 ? 1 : 0;
+                const bool mine = lane >= i && lane < i + per_stage && id >= 0;  // a page of this stage
+                const int copies = __popc(__ballot_sync(0xffffffffu, mine));
+                if (lane == 0) t2::mbar_arrive_expect_tx(full + slot, (uint32_t)(copies * 2 * p.page * D));
                 __syncwarp();
-                if (lane == 0) t2::mbar_arrive_expect_tx(full + slot, (uint32_t)(copies * 2 * piece * D));
-                __syncwarp();
-                for (int j = 0; j < per_stage; ++j) {
-                    const int pid = __shfl_sync(0xffffffffu, id, (i + j) & 31);
-                    if (lane == 0 && pid >= 0) {
-                        const int row = (int)((lo + (long long)st * kStepKeys + j * piece) % p.page);
-                        t2::tma_load_3d(kd + (size_t)j * piece * D, &p.tk, 0, row, pid * p.Hk + hk, full + slot);
-                        t2::tma_load_3d(kd + SM::kTile + (size_t)j * piece * D, &p.tv, 0, row,
-                                        pid * p.Hk + hk, full + slot);
-                    }
+                if (mine) {
+                    unsigned char* kd = sm + (size_t)slot * 2 * SM::kTile + (size_t)(lane - i) * p.page * D;
+                    t2::tma_load_3d(kd, &p.tk, 0, 0, id * p.Hk + hk, full + slot);
+                    t2::tma_load_3d(kd + SM::kTile, &p.tv, 0, 0, id * p.Hk + hk, full + slot);
                 }
+                __syncwarp();
             }
         }
         if (bad && lane == 0) atomicOr(&g_kv_timeouts, 1u);
@@ -324,23 +332,28 @@ __global__ void __launch_bounds__(kStepThreads) k_attn_step(const __grid_constan
         // each of them below before the block ends
     }
 
-    // ---- consumers
+    // ---- consumers: keys g and g + 8 of a group, heads 8 h + 2 c and + 1
     const int g = lane >> 2, c = lane & 3;
-    float m[2] = {-INFINITY, -INFINITY}, M[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
-    float acc[NT][4];
+    float m[HT][2], M[HT][2], l[HT][2];
+    float acc[HT][NT][4];  // channels g * D/8 + 2 t (0, 1) and + 1 (2, 3) of the two heads
 #pragma unroll
-    for (int t = 0; t < NT; ++t)
+    for (int h = 0; h < HT; ++h) {
+        m[h][0] = m[h][1] = M[h][0] = M[h][1] = -INFINITY;
+        l[h][0] = l[h][1] = 0.f;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) acc[t][i] = 0.f;
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) acc[h][t][i] = 0.f;
+    }
 
     if (warp < kStepWarps && nst > 0) {
-        // query fragments: rows g and g + 8; step s of the contraction takes channels
+        // query fragments of head 8 h + g: step s of the contraction takes channels
         // c * D/4 + 4 s .. + 3 of lane c
-        uint32_t qa[KSTEPS][4];
-        float qscale[2];
+        uint32_t qb[HT][KSTEPS][2];
+        float qscale[HT][2];
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-            const int head = g0 + g + 8 * r;
+        for (int h = 0; h < HT; ++h) {
+            const int head = g0 + 8 * h + g;
             float x[D / 4];
             float mx = 0.f;
             const bool on = head < G;
@@ -360,14 +373,16 @@ __global__ void __launch_bounds__(kStepThreads) k_attn_step(const __grid_constan
             if (mx > 0.f && mx <= 3.4e38f) frexpf(mx, &e);
             const int sh = 14 - e;  // in [-114, 163]: applied in two halves
             const float s1 = ldexpf(1.f, sh / 2), s2 = ldexpf(1.f, sh - sh / 2);
-            qscale[r] = p.scale_log2 / s1 / s2;
+            const float qs = p.scale_log2 / s1 / s2;
 #pragma unroll
-            for (int s = 0; s < KSTEPS; ++s) {
-                const __half2 u = __floats2half2_rn(x[4 * s] * s1 * s2, x[4 * s + 1] * s1 * s2);
-                const __half2 v = __floats2half2_rn(x[4 * s + 2] * s1 * s2, x[4 * s + 3] * s1 * s2);
-                qa[s][r] = *reinterpret_cast<const uint32_t*>(&u);
-                qa[s][2 + r] = *reinterpret_cast<const uint32_t*>(&v);
-            }
+            for (int i = 0; i < 2; ++i) qscale[h][i] = __shfl_sync(0xffffffffu, qs, 4 * (2 * c + i));
+#pragma unroll
+            for (int s = 0; s < KSTEPS; ++s)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const __half2 u = __floats2half2_rn(x[4 * s + 2 * i] * s1 * s2, x[4 * s + 2 * i + 1] * s1 * s2);
+                    qb[h][s][i] = *reinterpret_cast<const uint32_t*>(&u);
+                }
         }
 
         for (int st = 0; st < nst; ++st) {
@@ -379,99 +394,125 @@ __global__ void __launch_bounds__(kStepThreads) k_attn_step(const __grid_constan
             }
             const unsigned char* kt = sm + (size_t)slot * 2 * SM::kTile;
             const unsigned char* vt = kt + SM::kTile;
-            const StepMeta mt = meta[slot * 4 + warp];
-            if (mt.hi > mt.lo) {  // uniform in the warp
-                float s[2][4];
+            const StepMeta mt[2] = {meta[slot * kGroups + 2 * warp], meta[slot * kGroups + 2 * warp + 1]};
+            const bool part = mt[0].lo > 0 || mt[0].hi < 16 || mt[1].lo > 0 || mt[1].hi < 16;
+            if (mt[0].hi > mt[0].lo || mt[1].hi > mt[1].lo) {  // uniform in the warp
+                float s[2][HT][4];
 #pragma unroll
-                for (int n = 0; n < 2; ++n) {
-                    const int r = 16 * warp + 8 * n + g;
-                    s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.f;
+                for (int u = 0; u < 2; ++u) {
+#pragma unroll
+                    for (int h = 0; h < HT; ++h) s[u][h][0] = s[u][h][1] = s[u][h][2] = s[u][h][3] = 0.f;
+                    const int r = kWarpKeys * warp + 16 * u + g;
 #pragma unroll
                     for (int i = 0; i < D / 64; ++i) {
-                        const uint4 kw = *reinterpret_cast<const uint4*>(kt + step_off<D>(r, c * (D / 64) + i));
-                        const uint32_t w[4] = {kw.x, kw.y, kw.z, kw.w};
+                        const uint4 ka = *reinterpret_cast<const uint4*>(kt + step_off<D>(r, c * (D / 64) + i));
+                        const uint4 kb = *reinterpret_cast<const uint4*>(kt + step_off<D>(r + 8, c * (D / 64) + i));
+                        const uint32_t wa[4] = {ka.x, ka.y, ka.z, ka.w}, wb[4] = {kb.x, kb.y, kb.z, kb.w};
 #pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            mma_f16_16816(s[n], qa[4 * i + j], h2_from_e4m3(w[j]), h2_from_e4m3_hi(w[j]));
+                        for (int j = 0; j < 4; ++j) {
+                            const uint32_t a0 = h2_from_e4m3(wa[j]), a1 = h2_from_e4m3(wb[j]);
+                            const uint32_t a2 = h2_from_e4m3_hi(wa[j]), a3 = h2_from_e4m3_hi(wb[j]);
+#pragma unroll
+                            for (int h = 0; h < HT; ++h)
+                                mma_f16_16816(s[u][h], a0, a1, a2, a3, qb[h][4 * i + j][0], qb[h][4 * i + j][1]);
+                        }
                     }
                 }
-                // rows g (r = 0) and g + 8 (r = 1); keys 8 n + 2 c, + 1
-                float pw[2][4];
+                uint32_t pb[2][HT][2];  // weights as the output product takes them
 #pragma unroll
-                for (int r = 0; r < 2; ++r) {
-                    const float f = qscale[r] * mt.ks;
-                    float mx = -INFINITY;
+                for (int h = 0; h < HT; ++h) {
+                    // scores in base 2; does any outgrow its reference?
+                    bool grow = false;
 #pragma unroll
-                    for (int n = 0; n < 2; ++n)
+                    for (int i = 0; i < 2; ++i)
+#pragma unroll
+                        for (int u = 0; u < 2; ++u) {
+                            const float f = qscale[h][i] * mt[u].ks;
+#pragma unroll
+                            for (int r = 0; r < 2; ++r) {
+                                float& x = s[u][h][2 * r + i];
+                                x *= f;
+                                if (part && (g + 8 * r < mt[u].lo || g + 8 * r >= mt[u].hi)) x = -INFINITY;
+                                grow = grow || x > m[h][i] + kSlack || x + mt[u].lv > M[h][i] + kSlack;
+                            }
+                        }
+                    if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
                         for (int i = 0; i < 2; ++i) {
-                            const int key = 8 * n + 2 * c + i;
-                            float& x = s[n][2 * r + i];
-                            x = (key >= mt.lo && key < mt.hi) ? x * f : -INFINITY;
-                            mx = fmaxf(mx, x);
-                        }
-                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-                    const float mn = fmaxf(m[r], mx);
-                    const float ms = mn == -INFINITY ? 0.f : mn;
-                    l[r] *= ex2(m[r] - ms);
-                    m[r] = mn;
-                    const float Mn = fmaxf(M[r], mx + mt.lv);
-                    const float Ms = Mn == -INFINITY ? 0.f : Mn;
-                    if (__any_sync(0xffffffffu, Mn != M[r])) {
-                        const float a = ex2(M[r] - Ms);
+                            float a = fmaxf(s[0][h][i], s[0][h][2 + i]), d = fmaxf(s[1][h][i], s[1][h][2 + i]);
+                            float top = fmaxf(a, d), tv = fmaxf(a + mt[0].lv, d + mt[1].lv);
 #pragma unroll
-                        for (int t = 0; t < NT; ++t) {
-                            acc[t][2 * r] *= a;
-                            acc[t][2 * r + 1] *= a;
+                            for (int o = 4; o < 32; o <<= 1) {
+                                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+                                tv = fmaxf(tv, __shfl_xor_sync(0xffffffffu, tv, o));
+                            }
+                            const float mn = fmaxf(m[h][i], top), Mn = fmaxf(M[h][i], tv);
+                            l[h][i] *= mn == -INFINITY ? 1.f : ex2(m[h][i] - mn);
+                            const float f = Mn == -INFINITY ? 1.f : ex2(M[h][i] - Mn);
+                            m[h][i] = mn;
+                            M[h][i] = Mn;
+#pragma unroll
+                            for (int t = 0; t < NT; ++t) {
+                                acc[h][t][i] *= f;
+                                acc[h][t][2 + i] *= f;
+                            }
                         }
                     }
-                    M[r] = Mn;
-                    const float off = mt.lv - Ms + 15.f;
+                    float w[2][4];
 #pragma unroll
-                    for (int n = 0; n < 2; ++n)
+                    for (int i = 0; i < 2; ++i) {
+                        const float ms = m[h][i] == -INFINITY ? 0.f : m[h][i];
+                        const float Ms = M[h][i] == -INFINITY ? 0.f : M[h][i];
 #pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            const float x = s[n][2 * r + i];
-                            l[r] += ex2(x - ms);
-                            pw[n][2 * r + i] = ex2(x + off);
+                        for (int u = 0; u < 2; ++u)
+#pragma unroll
+                            for (int r = 0; r < 2; ++r) {
+                                const float x = s[u][h][2 * r + i];
+                                l[h][i] += ex2(x - ms);
+                                w[u][2 * r + i] = ex2(x + (mt[u].lv + (kWeightExp - Ms)));
+                            }
+                    }
+#pragma unroll
+                    for (int u = 0; u < 2; ++u)
+#pragma unroll
+                        for (int r = 0; r < 2; ++r) {
+                            const __half2 two = __floats2half2_rn(w[u][2 * r], w[u][2 * r + 1]);
+                            pb[u][h][r] = transpose8(*reinterpret_cast<const uint32_t*>(&two));
                         }
                 }
-                uint32_t pa[4];
+                // value codes of keys 2c, 2c+1, 2c+8, 2c+9, channels g * D/8 .. + D/8
 #pragma unroll
-                for (int n = 0; n < 2; ++n)
+                for (int u = 0; u < 2; ++u) {
+                    uint32_t w[4][D / 32];
 #pragma unroll
-                    for (int r = 0; r < 2; ++r) {
-                        const __half2 u = __floats2half2_rn(pw[n][2 * r], pw[n][2 * r + 1]);
-                        pa[2 * n + r] = *reinterpret_cast<const uint32_t*>(&u);
+                    for (int i = 0; i < 4; ++i) {
+                        const int kk = 2 * c + (i & 1) + 8 * (i >> 1);
+                        const int r = kWarpKeys * warp + 16 * u + kk;
+                        if (D == 128) {
+                            const uint4 x = *reinterpret_cast<const uint4*>(vt + step_off<D>(r, g));
+                            w[i][0] = x.x; w[i][1] = x.y; w[i][D / 32 - 2] = x.z; w[i][D / 32 - 1] = x.w;
+                        } else {
+                            const uint2 x = *reinterpret_cast<const uint2*>(vt + step_off<D>(r, g >> 1) + 8 * (g & 1));
+                            w[i][0] = x.x; w[i][1] = x.y;
+                        }
+                        // slots behind the sequence may hold anything: no code of theirs is used
+                        if (part && (kk < mt[u].lo || kk >= mt[u].hi)) {
+#pragma unroll
+                            for (int j = 0; j < D / 32; ++j) w[i][j] = 0u;
+                        }
                     }
-                // value codes of keys 2c, 2c+1, 2c+8, 2c+9, columns g * D/8 .. + D/8
-                uint32_t w[4][D / 32];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int kk = 2 * c + (i & 1) + 8 * (i >> 1);
-                    const int r = 16 * warp + kk;
-                    if (D == 128) {
-                        const uint4 u = *reinterpret_cast<const uint4*>(vt + step_off<D>(r, g));
-                        w[i][0] = u.x; w[i][1] = u.y; w[i][D / 32 - 2] = u.z; w[i][D / 32 - 1] = u.w;
-                    } else {
-                        const uint2 u = *reinterpret_cast<const uint2*>(vt + step_off<D>(r, g >> 1) + 8 * (g & 1));
-                        w[i][0] = u.x; w[i][1] = u.y;
+                    for (int j = 0; j < D / 32; ++j) {
+                        const uint32_t a0 = __byte_perm(w[0][j], w[1][j], 0x5140), a1 = __byte_perm(w[0][j], w[1][j], 0x7362);
+                        const uint32_t b0 = __byte_perm(w[2][j], w[3][j], 0x5140), b1 = __byte_perm(w[2][j], w[3][j], 0x7362);
+                        const uint32_t x[8] = {h2_from_e4m3(a0), h2_from_e4m3_hi(a0), h2_from_e4m3(b0), h2_from_e4m3_hi(b0),
+                                               h2_from_e4m3(a1), h2_from_e4m3_hi(a1), h2_from_e4m3(b1), h2_from_e4m3_hi(b1)};
+#pragma unroll
+                        for (int h = 0; h < HT; ++h) {
+                            mma_f16_16816(acc[h][2 * j], x[0], x[1], x[2], x[3], pb[u][h][0], pb[u][h][1]);
+                            mma_f16_16816(acc[h][2 * j + 1], x[4], x[5], x[6], x[7], pb[u][h][0], pb[u][h][1]);
+                        }
                     }
-                    // slots behind the sequence may hold anything: no code of theirs is used
-                    if (kk < mt.lo || kk >= mt.hi) {
-#pragma unroll
-                        for (int j = 0; j < D / 32; ++j) w[i][j] = 0u;
-                    }
-                }
-#pragma unroll
-                for (int j = 0; j < D / 32; ++j) {
-                    const uint32_t a0 = __byte_perm(w[0][j], w[1][j], 0x5140), a1 = __byte_perm(w[0][j], w[1][j], 0x7362);
-                    const uint32_t b0 = __byte_perm(w[2][j], w[3][j], 0x5140), b1 = __byte_perm(w[2][j], w[3][j], 0x7362);
-                    mma_f16_16816(acc[4 * j], pa, h2_from_e4m3(a0), h2_from_e4m3(b0));
-                    mma_f16_16816(acc[4 * j + 1], pa, h2_from_e4m3_hi(a0), h2_from_e4m3_hi(b0));
-                    mma_f16_16816(acc[4 * j + 2], pa, h2_from_e4m3(a1), h2_from_e4m3(b1));
-                    mma_f16_16816(acc[4 * j + 3], pa, h2_from_e4m3_hi(a1), h2_from_e4m3_hi(b1));
                 }
             }
             __syncwarp();
@@ -482,41 +523,45 @@ __global__ void __launch_bounds__(kStepThreads) k_attn_step(const __grid_constan
 
     // ---- the four warps' parts together: o = sum_w 2^(m_w - m) ..., through the ring's memory
     __syncthreads();
-    float* so = reinterpret_cast<float*>(sm);               // [warp][16][D]
-    float* sml = so + kStepWarps * kRows * D;               // [warp][16][2]: m, l
+    float* so = reinterpret_cast<float*>(sm);               // [warp][ROWS][D]
+    float* sml = so + kStepWarps * ROWS * D;                // [warp][ROWS][2]: m, l
     if (warp < kStepWarps) {
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-            l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
-            l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
-            // in units of 2^m: the codes' weights carry 2^(15 - M)
-            const float u = l[r] > 0.f ? ex2(M[r] - 15.f - m[r]) : 0.f;
-            float* row = so + (warp * kRows + g + 8 * r) * D;
+        for (int h = 0; h < HT; ++h)
 #pragma unroll
-            for (int t = 0; t < NT; ++t) {
-                row[(2 * c) * (D / 8) + t] = acc[t][2 * r] * u;
-                row[(2 * c + 1) * (D / 8) + t] = acc[t][2 * r + 1] * u;
+            for (int i = 0; i < 2; ++i) {
+                float sum = l[h][i];
+#pragma unroll
+                for (int o = 4; o < 32; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+                // in units of 2^m: the codes' weights carry 2^(7 - M)
+                const float u = sum > 0.f ? ex2(M[h][i] - kWeightExp - m[h][i]) : 0.f;
+                const int row = warp * ROWS + 8 * h + 2 * c + i;
+                float* o = so + row * D + g * (D / 8);
+#pragma unroll
+                for (int t = 0; t < NT; ++t) {
+                    o[2 * t] = acc[h][t][i] * u;
+                    o[2 * t + 1] = acc[h][t][2 + i] * u;
+                }
+                if (g == 0) {
+                    sml[row * 2] = m[h][i];
+                    sml[row * 2 + 1] = sum;
+                }
             }
-            if (c == 0) {
-                sml[(warp * kRows + g + 8 * r) * 2] = m[r];
-                sml[(warp * kRows + g + 8 * r) * 2 + 1] = l[r];
-            }
-        }
     }
     __syncthreads();
-    const int rows = min(kRows, G - g0);
+    const int rows = min(ROWS, G - g0);
     for (int i = threadIdx.x; i < rows * D; i += kStepThreads) {
         const int r = i / D, ch = i % D;
         float mm = -INFINITY;
 #pragma unroll
-        for (int w = 0; w < kStepWarps; ++w) mm = fmaxf(mm, sml[(w * kRows + r) * 2]);
+        for (int w = 0; w < kStepWarps; ++w) mm = fmaxf(mm, sml[(w * ROWS + r) * 2]);
         const float ms = mm == -INFINITY ? 0.f : mm;
         float sum = 0.f, o = 0.f;
 #pragma unroll
         for (int w = 0; w < kStepWarps; ++w) {
-            const float f = ex2(sml[(w * kRows + r) * 2] - ms);
-            sum += f * sml[(w * kRows + r) * 2 + 1];
-            o += f * so[(w * kRows + r) * D + ch];
+            const float f = ex2(sml[(w * ROWS + r) * 2] - ms);
+            sum += f * sml[(w * ROWS + r) * 2 + 1];
+            o += f * so[(w * ROWS + r) * D + ch];
         }
         o = sum > 0.f || sum != sum ? o / sum : 0.f;
         const long long head = (long long)b * p.Hq + (long long)hk * G + g0 + r;
@@ -563,8 +608,12 @@ cudaError_t launch_kv_append(const AppendArgs& a, int B, int d, bool bf16, cudaS
     return cudaGetLastError();
 }
 
+// Query heads of a block: 8 columns of the products, or 16 where the group has more.
+static int step_heads(int Hq, int Hk) { return Hq / Hk <= 8 ? 8 : kMaxRows; }
+
 int attn_step_splits(int B, int Hq, int Hk, int page, int max_pages) {
-    const long long units = (long long)B * Hk * ((Hq / Hk + kRows - 1) / kRows);
+    const int per = step_heads(Hq, Hk);
+    const long long units = (long long)B * Hk * ((Hq / Hk + per - 1) / per);
     const long long cap = (long long)page * max_pages;
     // enough blocks for the resident ones of 148 SMs, and none longer than 2048 keys, so
     // that one long sequence of a ragged batch does not run on after the others
@@ -582,30 +631,28 @@ size_t attn_step_ws_bytes(int B, int Hq, int Hk, int d, int page, int max_pages)
     return s == 1 ? 0 : (size_t)B * Hq * s * (d + 1) * 4;
 }
 
+template <int D, int HT>
+static cudaError_t step(const StepArgs& a, dim3 grid, cudaStream_t st) {
+    static std::atomic<uint64_t> done{0};
+    const cudaError_t err = allow_smem(k_attn_step<D, HT>, StepSmem<D>::kBytes, done);
+    if (err != cudaSuccess) return err;
+    MUIR_TIMED("k_attn_step", st, k_attn_step<D, HT><<<grid, kStepThreads, StepSmem<D>::kBytes, st>>>(a));
+    return cudaGetLastError();
+}
+
 cudaError_t launch_attn_step(StepArgs a, int B, int d, void* ws, cudaStream_t st) {
     a.splits = attn_step_splits(B, a.Hq, a.Hk, a.page, a.max_pages);
     a.min_keys = 256;
     a.part = static_cast<float*>(ws);
     a.part_lse = a.part + (size_t)B * a.Hq * a.splits * d;
-    const int piece = a.page < kStepKeys ? a.page : kStepKeys;
-    cudaError_t err = make_tmap_u8(&a.tk, a.k_pages, d, a.page, (uint64_t)a.num_pages * a.Hk, piece);
+    cudaError_t err = make_tmap_u8(&a.tk, a.k_pages, d, a.page, (uint64_t)a.num_pages * a.Hk, a.page);
     if (err != cudaSuccess) return err;
-    err = make_tmap_u8(&a.tv, a.v_pages, d, a.page, (uint64_t)a.num_pages * a.Hk, piece);
+    err = make_tmap_u8(&a.tv, a.v_pages, d, a.page, (uint64_t)a.num_pages * a.Hk, a.page);
     if (err != cudaSuccess) return err;
-    const int gt = (a.Hq / a.Hk + kRows - 1) / kRows;
-    const dim3 grid(a.splits, a.Hk * gt, B);
-    if (d == 128) {
-        static std::atomic<uint64_t> done{0};
-        err = allow_smem(k_attn_step<128>, StepSmem<128>::kBytes, done);
-        if (err != cudaSuccess) return err;
-        MUIR_TIMED("k_attn_step", st, k_attn_step<128><<<grid, kStepThreads, StepSmem<128>::kBytes, st>>>(a));
-    } else {
-        static std::atomic<uint64_t> done{0};
-        err = allow_smem(k_attn_step<64>, StepSmem<64>::kBytes, done);
-        if (err != cudaSuccess) return err;
-        MUIR_TIMED("k_attn_step", st, k_attn_step<64><<<grid, kStepThreads, StepSmem<64>::kBytes, st>>>(a));
-    }
-    err = cudaGetLastError();
+    const int per = step_heads(a.Hq, a.Hk);
+    const dim3 grid(a.splits, a.Hk * ((a.Hq / a.Hk + per - 1) / per), B);
+    if (per == 8) err = d == 128 ? step<128, 1>(a, grid, st) : step<64, 1>(a, grid, st);
+    else err = d == 128 ? step<128, 2>(a, grid, st) : step<64, 2>(a, grid, st);
     if (err != cudaSuccess || a.splits == 1) return err;
     if (d == 128)
         MUIR_TIMED("k_attn_step_join", st, k_attn_step_join<128><<<B * a.Hq, 128, 0, st>>>(
