@@ -28,7 +28,7 @@ __device__ unsigned int g_kv_timeouts;
 
 namespace {
 
-constexpr int kAppThreads = 128;
+constexpr int kAppThreads = 256;
 
 __device__ __forceinline__ void kv_unpack(const uint4& a, float* v, float) {
     v[0] = __uint_as_float(a.x); v[1] = __uint_as_float(a.y);
@@ -65,7 +65,10 @@ __device__ __forceinline__ float scale_for(float amax) {
 // One block per (page a sequence's new tokens touch, head, keys or values): the new
 // rows' largest finite magnitude, the page's scale, held rows encoded again if the
 // scale grew, new rows encoded.  Rows of the page behind the new tokens stay as they are.
-template <typename T, int D>
+// The rows are read once, NV vectors of 16 bytes a thread, all in flight together, and
+// wait in registers for the scale (read twice through a loop instead, 27000 tokens of 4
+// heads of 128 took 15 us where this takes 11).
+template <typename T, int D, int NV>
 __global__ void __launch_bounds__(kAppThreads) k_kv_append(AppendArgs p) {
     constexpr int V = 16 / (int)sizeof(T);  // channels per vector
     constexpr int PER_ROW = D / V;
@@ -81,23 +84,29 @@ __global__ void __launch_bounds__(kAppThreads) k_kv_append(AppendArgs p) {
     const int hi = (int)min((long long)count, page0 + p.page - start);
     if (lo >= hi || slot >= p.max_pages) return;
     const int id = p.table[(long long)b * p.max_pages + slot];
-    if (id < 0 || id >= p.num_pages) return;
 
-    const T* src = static_cast<const T*>(which ? p.v : p.k) +
-                   ((long long)b * p.T + lo) * (which ? p.v_ld : p.k_ld) + (long long)h * D;
     const long long ld = which ? p.v_ld : p.k_ld;
+    const T* src = static_cast<const T*>(which ? p.v : p.k) + ((long long)b * p.T + lo) * ld + (long long)h * D;
+    const int items = (hi - lo) * PER_ROW;
+    uint4 x[NV];
+#pragma unroll
+    for (int n = 0; n < NV; ++n) {
+        const int i = n * kAppThreads + (int)threadIdx.x;
+        x[n] = make_uint4(0u, 0u, 0u, 0u);
+        if (i < items) x[n] = *reinterpret_cast<const uint4*>(src + (i / PER_ROW) * ld + (i % PER_ROW) * V);
+    }
+    if (id < 0 || id >= p.num_pages) return;  // the whole block
     unsigned char* dst = static_cast<unsigned char*>(which ? p.v_pages : p.k_pages) +
                          ((long long)id * p.Hk + h) * p.page * D;
     float* scale = (which ? p.v_scale : p.k_scale) + (long long)id * p.Hk + h;
     const int held = (int)(start + lo - page0);  // rows of the page before the new ones
-    const int items = (hi - lo) * PER_ROW;
     const float old = held > 0 ? *scale : 0.f;
 
     float amax = 0.f;
-    for (int i = threadIdx.x; i < items; i += kAppThreads) {
-        const int r = i / PER_ROW, c = i % PER_ROW;
+#pragma unroll
+    for (int n = 0; n < NV; ++n) {
         float v[V];
-        kv_unpack(*reinterpret_cast<const uint4*>(src + r * ld + c * V), v, T());
+        kv_unpack(x[n], v, T());
 #pragma unroll
         for (int j = 0; j < V; ++j) {
             const float a = fabsf(v[j]);
@@ -119,21 +128,23 @@ __global__ void __launch_bounds__(kAppThreads) k_kv_append(AppendArgs p) {
         const float ratio = old / now;
         for (int i = threadIdx.x; i < held * (D / 4); i += kAppThreads) {
             uint32_t* w = reinterpret_cast<uint32_t*>(dst) + i;
-            const uint32_t x = *w;
-            const float2 a = from_e4m3x2(x & 0xffffu), c = from_e4m3x2(x >> 16);
+            const uint32_t y = *w;
+            const float2 a = from_e4m3x2(y & 0xffffu), c = from_e4m3x2(y >> 16);
             *w = e4m3x2(a.x * ratio, a.y * ratio) | (e4m3x2(c.x * ratio, c.y * ratio) << 16);
         }
     }
-    for (int i = threadIdx.x; i < items; i += kAppThreads) {
-        const int r = i / PER_ROW, c = i % PER_ROW;
+#pragma unroll
+    for (int n = 0; n < NV; ++n) {
+        const int i = n * kAppThreads + (int)threadIdx.x;
+        if (i >= items) break;
         float v[V];
-        kv_unpack(*reinterpret_cast<const uint4*>(src + r * ld + c * V), v, T());
+        kv_unpack(x[n], v, T());
         uint32_t w[V / 4];
 #pragma unroll
         for (int j = 0; j < V / 4; ++j)
             w[j] = e4m3x2(v[4 * j] * inv, v[4 * j + 1] * inv) |
                    (e4m3x2(v[4 * j + 2] * inv, v[4 * j + 3] * inv) << 16);
-        uint32_t* o = reinterpret_cast<uint32_t*>(dst + (long long)(held + r) * D + c * V);
+        uint32_t* o = reinterpret_cast<uint32_t*>(dst + (long long)(held + i / PER_ROW) * D + (i % PER_ROW) * V);
         if (V == 8)
             *reinterpret_cast<uint2*>(o) = make_uint2(w[0], w[V / 4 - 1]);
         else
@@ -151,6 +162,7 @@ constexpr int kWarpKeys = kStepKeys / kStepWarps;
 constexpr int kStepThreads = 32 * (kStepWarps + 1);
 constexpr int kStepStages = 3;
 constexpr int kGroups = kStepKeys / 16;    // groups of 16 keys, within one page each
+constexpr int kU = kWarpKeys / 16;         // a warp's
 constexpr int kMaxRows = 16;               // query heads of a block
 constexpr float kSlack = 8.f;              // log2 of how far a weight may exceed 1
 constexpr float kWeightExp = 7.f;          // fp16 weights are 2^(score - reference + 7) <= 2^15
@@ -267,7 +279,7 @@ __global__ void __launch_bounds__(kStepThreads, HT == 1 ? 2 : 1) k_attn_step(con
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < kStepStages; ++i) {
-            t2::mbar_init(full + i, 1);
+            t2::mbar_init(full + i, 2);  // the copies and the metadata
             t2::mbar_init(empty + i, kStepWarps);
         }
         t2::fence_barrier_init();
@@ -301,6 +313,18 @@ __global__ void __launch_bounds__(kStepThreads, HT == 1 ? 2 : 1) k_attn_step(con
                         break;
                     }
                 }
+                // the copies first: they need the page ids only, and are on their way while
+                // the scales still are
+                const bool mine = lane >= i && lane < i + per_stage && id >= 0;  // a page of this stage
+                const int copies = __popc(__ballot_sync(0xffffffffu, mine));
+                if (lane == 0) t2::mbar_arrive_expect_tx(full + slot, (uint32_t)(copies * 2 * p.page * D));
+                __syncwarp();
+                if (mine) {
+                    unsigned char* kd = sm + (size_t)slot * 2 * SM::kTile + (size_t)(lane - i) * p.page * D;
+                    t2::tma_load_3d(kd, &p.tk, 0, 0, id * p.Hk + hk, full + slot);
+                    t2::tma_load_3d(kd + SM::kTile, &p.tv, 0, 0, id * p.Hk + hk, full + slot);
+                }
+                __syncwarp();
                 // metadata of the stage's groups
                 const int src = i + (lane * 16) / p.page;
                 const int gid = __shfl_sync(0xffffffffu, id, src & 31);
@@ -315,16 +339,8 @@ __global__ void __launch_bounds__(kStepThreads, HT == 1 ? 2 : 1) k_attn_step(con
                     m.hi = gid < 0 ? 0 : (int)max(0LL, min(16LL, hi - k0));
                     meta[slot * kGroups + lane] = m;
                 }
-                const bool mine = lane >= i && lane < i + per_stage && id >= 0;  // a page of this stage
-                const int copies = __popc(__ballot_sync(0xffffffffu, mine));
-                if (lane == 0) t2::mbar_arrive_expect_tx(full + slot, (uint32_t)(copies * 2 * p.page * D));
                 __syncwarp();
-                if (mine) {
-                    unsigned char* kd = sm + (size_t)slot * 2 * SM::kTile + (size_t)(lane - i) * p.page * D;
-                    t2::tma_load_3d(kd, &p.tk, 0, 0, id * p.Hk + hk, full + slot);
-                    t2::tma_load_3d(kd + SM::kTile, &p.tv, 0, 0, id * p.Hk + hk, full + slot);
-                }
-                __syncwarp();
+                if (lane == 0) mbar_arrive(full + slot);
             }
         }
         if (bad && lane == 0) atomicOr(&g_kv_timeouts, 1u);
@@ -394,12 +410,18 @@ __global__ void __launch_bounds__(kStepThreads, HT == 1 ? 2 : 1) k_attn_step(con
             }
             const unsigned char* kt = sm + (size_t)slot * 2 * SM::kTile;
             const unsigned char* vt = kt + SM::kTile;
-            const StepMeta mt[2] = {meta[slot * kGroups + 2 * warp], meta[slot * kGroups + 2 * warp + 1]};
-            const bool part = mt[0].lo > 0 || mt[0].hi < 16 || mt[1].lo > 0 || mt[1].hi < 16;
-            if (mt[0].hi > mt[0].lo || mt[1].hi > mt[1].lo) {  // uniform in the warp
-                float s[2][HT][4];
+            StepMeta mt[kU];
+            bool part = false, any = false;  // uniform in the warp
 #pragma unroll
-                for (int u = 0; u < 2; ++u) {
+            for (int u = 0; u < kU; ++u) {
+                mt[u] = meta[slot * kGroups + kU * warp + u];
+                part = part || mt[u].lo > 0 || mt[u].hi < 16;
+                any = any || mt[u].hi > mt[u].lo;
+            }
+            if (any) {
+                float s[kU][HT][4];
+#pragma unroll
+                for (int u = 0; u < kU; ++u) {
 #pragma unroll
                     for (int h = 0; h < HT; ++h) s[u][h][0] = s[u][h][1] = s[u][h][2] = s[u][h][3] = 0.f;
                     const int r = kWarpKeys * warp + 16 * u + g;
@@ -418,7 +440,7 @@ __global__ void __launch_bounds__(kStepThreads, HT == 1 ? 2 : 1) k_attn_step(con
                         }
                     }
                 }
-                uint32_t pb[2][HT][2];  // weights as the output product takes them
+                uint32_t pb[kU][HT][2];  // weights as the output product takes them
 #pragma unroll
                 for (int h = 0; h < HT; ++h) {
                     // scores in base 2; does any outgrow its reference?
@@ -426,7 +448,7 @@ __global__ void __launch_bounds__(kStepThreads, HT == 1 ? 2 : 1) k_attn_step(con
 #pragma unroll
                     for (int i = 0; i < 2; ++i)
 #pragma unroll
-                        for (int u = 0; u < 2; ++u) {
+                        for (int u = 0; u < kU; ++u) {
                             const float f = qscale[h][i] * mt[u].ks;
 #pragma unroll
                             for (int r = 0; r < 2; ++r) {
@@ -439,8 +461,13 @@ __global__ void __launch_bounds__(kStepThreads, HT == 1 ? 2 : 1) k_attn_step(con
                     if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
                         for (int i = 0; i < 2; ++i) {
-                            float a = fmaxf(s[0][h][i], s[0][h][2 + i]), d = fmaxf(s[1][h][i], s[1][h][2 + i]);
-                            float top = fmaxf(a, d), tv = fmaxf(a + mt[0].lv, d + mt[1].lv);
+                            float top = -INFINITY, tv = -INFINITY;
+#pragma unroll
+                            for (int u = 0; u < kU; ++u) {
+                                const float a = fmaxf(s[u][h][i], s[u][h][2 + i]);
+                                top = fmaxf(top, a);
+                                tv = fmaxf(tv, a + mt[u].lv);
+                            }
 #pragma unroll
                             for (int o = 4; o < 32; o <<= 1) {
                                 top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
@@ -458,13 +485,13 @@ __global__ void __launch_bounds__(kStepThreads, HT == 1 ? 2 : 1) k_attn_step(con
                             }
                         }
                     }
-                    float w[2][4];
+                    float w[kU][4];
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
                         const float ms = m[h][i] == -INFINITY ? 0.f : m[h][i];
                         const float Ms = M[h][i] == -INFINITY ? 0.f : M[h][i];
 #pragma unroll
-                        for (int u = 0; u < 2; ++u)
+                        for (int u = 0; u < kU; ++u)
 #pragma unroll
                             for (int r = 0; r < 2; ++r) {
                                 const float x = s[u][h][2 * r + i];
@@ -473,7 +500,7 @@ __global__ void __launch_bounds__(kStepThreads, HT == 1 ? 2 : 1) k_attn_step(con
                             }
                     }
 #pragma unroll
-                    for (int u = 0; u < 2; ++u)
+                    for (int u = 0; u < kU; ++u)
 #pragma unroll
                         for (int r = 0; r < 2; ++r) {
                             const __half2 two = __floats2half2_rn(w[u][2 * r], w[u][2 * r + 1]);
@@ -482,7 +509,7 @@ __global__ void __launch_bounds__(kStepThreads, HT == 1 ? 2 : 1) k_attn_step(con
                 }
                 // value codes of keys 2c, 2c+1, 2c+8, 2c+9, channels g * D/8 .. + D/8
 #pragma unroll
-                for (int u = 0; u < 2; ++u) {
+                for (int u = 0; u < kU; ++u) {
                     uint32_t w[4][D / 32];
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
@@ -596,16 +623,21 @@ __global__ void __launch_bounds__(D) k_attn_step_join(const float* part, const f
 
 }  // namespace
 
+template <typename T, int D>
+static cudaError_t append(const AppendArgs& a, dim3 grid, cudaStream_t st) {
+    // vectors a thread holds of the most rows that one page takes in this call
+    const int rows = a.T < a.page ? a.T : a.page;
+    const int nv = (rows * D * (int)sizeof(T) / 16 + kAppThreads - 1) / kAppThreads;
+    if (nv <= 1) MUIR_TIMED("k_kv_append", st, k_kv_append<T, D, 1><<<grid, kAppThreads, 0, st>>>(a));
+    else if (nv <= 4) MUIR_TIMED("k_kv_append", st, k_kv_append<T, D, 4><<<grid, kAppThreads, 0, st>>>(a));
+    else MUIR_TIMED("k_kv_append", st, k_kv_append<T, D, 16><<<grid, kAppThreads, 0, st>>>(a));
+    return cudaGetLastError();
+}
+
 cudaError_t launch_kv_append(const AppendArgs& a, int B, int d, bool bf16, cudaStream_t st) {
     const dim3 grid((a.T + a.page - 2) / a.page + 1, a.Hk, 2 * B);
-    if (bf16) {
-        if (d == 128) MUIR_TIMED("k_kv_append", st, k_kv_append<__nv_bfloat16, 128><<<grid, kAppThreads, 0, st>>>(a));
-        else MUIR_TIMED("k_kv_append", st, k_kv_append<__nv_bfloat16, 64><<<grid, kAppThreads, 0, st>>>(a));
-    } else {
-        if (d == 128) MUIR_TIMED("k_kv_append", st, k_kv_append<float, 128><<<grid, kAppThreads, 0, st>>>(a));
-        else MUIR_TIMED("k_kv_append", st, k_kv_append<float, 64><<<grid, kAppThreads, 0, st>>>(a));
-    }
-    return cudaGetLastError();
+    if (bf16) return d == 128 ? append<__nv_bfloat16, 128>(a, grid, st) : append<__nv_bfloat16, 64>(a, grid, st);
+    return d == 128 ? append<float, 128>(a, grid, st) : append<float, 64>(a, grid, st);
 }
 
 // Query heads of a block: 8 columns of the products, or 16 where the group has more.
@@ -645,9 +677,9 @@ cudaError_t launch_attn_step(StepArgs a, int B, int d, void* ws, cudaStream_t st
     a.min_keys = 256;
     a.part = static_cast<float*>(ws);
     a.part_lse = a.part + (size_t)B * a.Hq * a.splits * d;
-    cudaError_t err = make_tmap_u8(&a.tk, a.k_pages, d, a.page, (uint64_t)a.num_pages * a.Hk, a.page);
+    cudaError_t err = make_tmap_u8(&a.tk, a.k_pages, d, a.page, (uint64_t)a.num_pages * a.Hk, a.page < kStepKeys ? a.page : kStepKeys);
     if (err != cudaSuccess) return err;
-    err = make_tmap_u8(&a.tv, a.v_pages, d, a.page, (uint64_t)a.num_pages * a.Hk, a.page);
+    err = make_tmap_u8(&a.tv, a.v_pages, d, a.page, (uint64_t)a.num_pages * a.Hk, a.page < kStepKeys ? a.page : kStepKeys);
     if (err != cudaSuccess) return err;
     const int per = step_heads(a.Hq, a.Hk);
     const dim3 grid(a.splits, a.Hk * ((a.Hq / a.Hk + per - 1) / per), B);

@@ -28,7 +28,7 @@ namespace muir {
 namespace {
 
 constexpr int kRotThreads = 256;
-constexpr int kRotItems = 4;       // items of two 16-byte vectors in flight per thread
+constexpr int kRotItems = 2;       // items of two 16-byte vectors in flight per thread
 constexpr int kRotTabPairs = 1024; // (token, pair) entries of the table
 
 __device__ __forceinline__ void rot_unpack(const uint4& a, float* v, float) {
@@ -58,13 +58,18 @@ __device__ __forceinline__ uint4 rot_pack(const float* v, __nv_bfloat16) {
 }
 
 template <typename T, bool INTER>
-__global__ void __launch_bounds__(kRotThreads, 4) k_rotary(RotaryArgs p) {
+__global__ void __launch_bounds__(kRotThreads, 5) k_rotary(RotaryArgs p) {
     constexpr int V = 16 / (int)sizeof(T);  // channels per vector
-    __shared__ float2 tab[kRotTabPairs];    // (m cos t, m sin t) of [token][pair]
+    // m cos t, then m sin t, of a token's pairs, four to a vector: [token][2 V / 4][item],
+    // where an item's V pairs are the same in every head; lanes of neighbouring items read
+    // neighbouring vectors
+    constexpr int Q = V / 4;
+    __shared__ float4 tab[kRotTabPairs / 2];
     const int half = p.rot / 2;
-    const int per_head = p.d / (2 * V);     // items of a head
+    const int head_shift = 31 - __clz(p.d / (2 * V));  // log2 of the items of a head
     const int rot_items = p.rot / (2 * V);
-    const int per_tok = (p.Hq + p.Hk) * per_head;
+    const int heads = p.Hq + p.Hk;
+    const int per_tok = heads << head_shift;
     const long long tok0 = (long long)blockIdx.x * p.tokens_per_block;
     const int ntok = (int)min((long long)p.tokens_per_block, p.tokens - tok0);
     const int total = ntok * per_tok;
@@ -73,24 +78,24 @@ __global__ void __launch_bounds__(kRotThreads, 4) k_rotary(RotaryArgs p) {
     for (int base = 0; base < total; base += kRotThreads * kRotItems) {
         uint4 x[kRotItems][2];
         T* dst[kRotItems];
-        int ti[kRotItems];   // table index of the item's first pair, -1: pass through, -2: none
+        int ti[kRotItems];   // the item's place in the table, -1: pass through, -2: none
         int gap[kRotItems];  // channels between the item's two vectors
 #pragma unroll
         for (int u = 0; u < kRotItems; ++u) {
             const int it = base + u * kRotThreads + (int)threadIdx.x;
             ti[u] = -2;
             if (it >= total) continue;
-            const int t = it / per_tok;
-            int r = it - t * per_tok;
-            const int h = r / per_head;
-            const int c = r - h * per_head;
+            const int th = it >> head_shift;
+            const int t = (int)((unsigned)th / (unsigned)heads);
+            const int h = th - t * heads;
+            const int c = it & ((1 << head_shift) - 1);
             const bool is_q = h < p.Hq;
             const int hh = is_q ? h : h - p.Hq;
             int ch;
             if (c < rot_items) {
                 ch = INTER ? c * 2 * V : c * V;
                 gap[u] = INTER ? V : half;
-                ti[u] = t * half + (INTER ? c * V : c * V);
+                ti[u] = t * (2 * Q) * rot_items + c;
             } else {
                 ch = c * 2 * V;
                 gap[u] = V;
@@ -108,14 +113,16 @@ __global__ void __launch_bounds__(kRotThreads, 4) k_rotary(RotaryArgs p) {
         }
         if (!have_tab) {  // block-uniform
             for (int e = threadIdx.x; e < ntok * half; e += kRotThreads) {
-                const int t = e / half;
+                const int t = e / half, i = e - t * half;
                 const long long row = tok0 + t;
                 const int pos = p.positions ? p.positions[row] : (int)(row % p.T);
-                const double turns = (double)pos * p.inv_freq[e - t * half] * 0.15915494309189535;
+                const double turns = (double)pos * p.inv_freq[i] * 0.15915494309189535;
                 const float w = (float)(2.0 * (turns - rint(turns)));  // half turns in [-1, 1]
                 float sn, cs;
                 sincospif(w, &sn, &cs);
-                tab[e] = make_float2(cs * p.mscale, (p.inverse ? -sn : sn) * p.mscale);
+                const int at = (t * (2 * Q) + (i % V) / 4) * rot_items + i / V;
+                reinterpret_cast<float*>(tab + at)[i % 4] = cs * p.mscale;
+                reinterpret_cast<float*>(tab + at + Q * rot_items)[i % 4] = (p.inverse ? -sn : sn) * p.mscale;
             }
             __syncthreads();
             have_tab = true;
@@ -127,13 +134,17 @@ __global__ void __launch_bounds__(kRotThreads, 4) k_rotary(RotaryArgs p) {
                 float a[2 * V], y[2 * V];
                 rot_unpack(x[u][0], a, T());
                 rot_unpack(x[u][1], a + V, T());
-                const float2* cs = tab + ti[u];
 #pragma unroll
-                for (int i = 0; i < V; ++i) {
-                    const float2 w = cs[i];
-                    const int ia = INTER ? 2 * i : i, ib = INTER ? 2 * i + 1 : i + V;
-                    y[ia] = a[ia] * w.x - a[ib] * w.y;
-                    y[ib] = a[ib] * w.x + a[ia] * w.y;
+                for (int q = 0; q < Q; ++q) {
+                    const float4 c4 = tab[ti[u] + q * rot_items], s4 = tab[ti[u] + (Q + q) * rot_items];
+                    const float cs[4] = {c4.x, c4.y, c4.z, c4.w}, sn[4] = {s4.x, s4.y, s4.z, s4.w};
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) {
+                        const int i = 4 * q + x;
+                        const int ia = INTER ? 2 * i : i, ib = INTER ? 2 * i + 1 : i + V;
+                        y[ia] = a[ia] * cs[x] - a[ib] * sn[x];
+                        y[ib] = a[ib] * cs[x] + a[ia] * sn[x];
+                    }
                 }
                 x[u][0] = rot_pack(y, T());
                 x[u][1] = rot_pack(y + V, T());
