@@ -127,39 +127,6 @@ __device__ __forceinline__ bool load_pair(unsigned char* dst, const CUtensorMap*
     return true;
 }
 
-// 128 lanes x D columns of tensor memory, times f, as bf16 rows of a token-major tensor
-// [rows][heads][D], through a tile of shared memory that nothing reads any more.  Four warps
-// (`wg` = 0 or 1 picks which of the block's two groups), rows < `rows` only.
-template <int D>
-__device__ __forceinline__ void store_rows(uint32_t tsrc, float f, bool any, unsigned char* tile,
-                                           __nv_bfloat16* dst, long long ld, int rows) {
-    const int w = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31, r = 32 * w + lane;
-    const uint32_t lane0 = (uint32_t)w << 21;
-#pragma unroll
-    for (int x = 0; x < D; x += 32) {
-        float v[32];
-        if (any) {
-            tmem_ld32(tsrc + lane0 + x, v);
-            tmem_wait_ld();
-        } else {
-#pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] = 0.f;
-        }
-#pragma unroll
-        for (int i = 0; i < 32; ++i) v[i] *= f;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) st_chunk16<true>(tile, r, x / 8 + i, v + 8 * i);
-    }
-    __syncwarp();
-    constexpr int CH = D / 8;
-    for (int i = lane; i < 32 * CH; i += 32) {
-        const int rr = 32 * w + i / CH, ch = i % CH;
-        if (rr < rows)
-            *reinterpret_cast<uint4*>(dst + (long long)rr * ld + 8 * ch) =
-                *reinterpret_cast<const uint4*>(tile + t16_off(rr, ch));
-    }
-}
-
 template <int NS>
 struct DkvBars {
     uint64_t res_full;                 // the resident tiles

@@ -39,6 +39,7 @@ namespace {
 constexpr int kThreads = 352;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
+constexpr int kSMs = 148;
 constexpr float kSlack = 8.f;  // log2 of how far a weight may exceed 1
 
 struct FwdParams {
@@ -47,7 +48,7 @@ struct FwdParams {
     float* lse;
     long long lse_seq, lse_head;
     float scale_log2;
-    int Hq, Hk, causal, window, n;
+    int Hq, Hk, causal, window, tiles, n;  // tiles: query tiles of a block
     Seq seq[kMaxSeqs];
 };
 
@@ -79,8 +80,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fwd(const __grid_constant_
     const int blk = blockIdx.x / p.Hq, h = blockIdx.x % p.Hq;
     const Seq sq = p.seq[find_seq(p.seq, p.n, blk)];
     // the longest rows of a causal sequence first
-    const int nblk = (sq.lq + 2 * kTile - 1) / (2 * kTile);
-    const int qb = nblk - 1 - (blk - sq.block0);
+    const int nblk = (sq.lq + p.tiles * kTile - 1) / (p.tiles * kTile);
+    const int qt = (nblk - 1 - (blk - sq.block0)) * p.tiles;  // its first query tile
     const int hk = h / (p.Hq / p.Hk);
     const int off = sq.lk - sq.lq;
 
@@ -88,20 +89,28 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fwd(const __grid_constant_
     int lo[2], hi[2];
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
-        const int r0 = (2 * qb + t) * kTile, r1 = min(r0 + kTile, sq.lq) - 1;  // its rows [r0, r1]
+        const int r0 = (qt + t) * kTile, r1 = min(r0 + kTile, sq.lq) - 1;  // its rows [r0, r1]
         int last = sq.lk - 1, first = 0;
         if (p.causal) last = min(last, r1 + off);
         if (p.window) first = max(first, r0 + off - p.window + 1);
         hi[t] = last < 0 ? 0 : last / kTile + 1;
         lo[t] = first / kTile;
-        if (r0 >= sq.lq || last < first) hi[t] = lo[t] = 0;
+        if (t >= p.tiles || r0 >= sq.lq || last < first) hi[t] = lo[t] = 0;
     }
     const bool on0 = hi[0] > lo[0], on1 = hi[1] > lo[1];
     const int jlo = on0 ? (on1 ? min(lo[0], lo[1]) : lo[0]) : lo[1];
     const int jhi = on0 ? (on1 ? max(hi[0], hi[1]) : hi[0]) : hi[1];
     const int loads = 2 * (jhi - jlo);  // K, V of each key tile in turn
 
-    if (threadIdx.x == 0) {
+    // The loading warp sets the barriers up and sends its first loads off before the block
+    // meets: they take longer than everything else that comes before the first product.
+    auto load = [&](int i) {
+        const int st = i % NS;
+        mbar_arrive_expect_tx(kv_full + st, SM::kTileBytes);
+        load_tile<D>(sm + SM::kRing + st * SM::kTileBytes, (i & 1) ? &p.tv : &p.tk, hk,
+                     sq.k0 + (jlo + i / 2) * kTile, kv_full + st);
+    };
+    if (threadIdx.x == 32 * 10) {
         for (int i = 0; i < 2; ++i) {
             mbar_init(q_full + i, 1);
             mbar_init(s_full + i, 1);
@@ -115,6 +124,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fwd(const __grid_constant_
         }
         mbar_init(tail_bar, 1);
         fence_barrier_init();
+        for (int t = 0; t < 2; ++t)
+            if (hi[t] > lo[t]) {
+                mbar_arrive_expect_tx(q_full + t, SM::kTileBytes);
+                load_tile<D>(sm + t * SM::kTileBytes, &p.tq, h, sq.q0 + (qt + t) * kTile, q_full + t);
+                if (t == 0 || !on0) load(0);
+            }
     }
     if (warp == 8) tmem_alloc(tmem_slot, 512);
     tc_fence_before();
@@ -130,14 +145,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fwd(const __grid_constant_
 
     if (warp == 10) {
         // ---------------------------------------------------------------- loads
-        if (lane == 0) {
-            for (int t = 0; t < 2; ++t)
-                if (hi[t] > lo[t]) {
-                    mbar_arrive_expect_tx(q_full + t, SM::kTileBytes);
-                    load_tile<D>(sm + t * SM::kTileBytes, &p.tq, h, sq.q0 + (2 * qb + t) * kTile, q_full + t);
-                }
-        }
-        for (int i = 0; i < loads; ++i) {
+        for (int i = 1; i < loads; ++i) {  // the first is on its way
             const int st = i % NS, j = jlo + i / 2;
             if (i >= NS) {
                 const bool ok = mbar_wait(kv_empty + st, (i / NS - 1) & 1);
@@ -151,13 +159,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fwd(const __grid_constant_
             // The value rows behind the sequence's last key belong to another sequence or to
             // nobody: their weight is zero, which a NaN or an infinity there would survive.
             const bool tail = (i & 1) && rows < kTile;
-            uint64_t* bar = tail ? tail_bar : kv_full + st;
-            if (lane == 0) {
-                mbar_arrive_expect_tx(bar, SM::kTileBytes);
-                load_tile<D>(dst, (i & 1) ? &p.tv : &p.tk, hk, sq.k0 + j * kTile, bar);
-            }
-            __syncwarp();
+            if (lane == 0 && !tail) load(i);
             if (tail) {
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(tail_bar, SM::kTileBytes);
+                    load_tile<D>(dst, &p.tv, hk, sq.k0 + j * kTile, tail_bar);
+                }
+                __syncwarp();
                 const bool ok = mbar_wait(tail_bar, 0);
                 if (!__all_sync(0xffffffffu, ok)) {
                     bad = true;
@@ -231,13 +239,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fwd(const __grid_constant_
     } else {
         // ---------------------------------------------------------------- softmax
         const int t = warp >> 2;
-        const int row = (2 * qb + t) * kTile + (threadIdx.x & 127);  // of the sequence
+        const int row = (qt + t) * kTile + (threadIdx.x & 127);  // of the sequence
         const uint32_t lane0 = (uint32_t)(warp & 3) << 21;           // this warp's TMEM lanes
         const int at = row + off;
         const int kmax = p.causal ? min(sq.lk - 1, at) : sq.lk - 1;  // visible keys [kmin, kmax]
         const int kmin = p.window ? at - p.window + 1 : 0;
         // of the tile's first and last row: which key tiles need no mask
-        const int r0 = (2 * qb + t) * kTile;
+        const int r0 = (qt + t) * kTile;
         const int all_max = p.causal ? min(sq.lk - 1, r0 + off) : sq.lk - 1;
         const int all_min = p.window ? r0 + kTile - 1 + off - p.window + 1 : 0;
         float m = -INFINITY, l = 0.f;  // m in units of score * scale * log2 e
@@ -260,11 +268,18 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fwd(const __grid_constant_
             const int k0 = j * kTile;
             if (k0 + kTile - 1 > all_max || k0 < all_min) {
                 const int a = kmin - k0, b = kmax - k0;
+                if (k0 + kTile - 1 > all_max) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
+                    for (int i = 0; i < 4; ++i)
 #pragma unroll
-                    for (int x = 0; x < 32; ++x)
-                        s[i][x] = (32 * i + x >= a && 32 * i + x <= b) ? s[i][x] : -INFINITY;
+                        for (int x = 0; x < 32; ++x) s[i][x] = 32 * i + x <= b ? s[i][x] : -INFINITY;
+                }
+                if (k0 < all_min) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+#pragma unroll
+                        for (int x = 0; x < 32; ++x) s[i][x] = 32 * i + x >= a ? s[i][x] : -INFINITY;
+                }
             }
             float mx[4];
 #pragma unroll
@@ -334,35 +349,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fwd(const __grid_constant_
         }
         if (bad && lane == 0) atomicOr(&g_fwd_timeouts, 4u);
         const float inv = l == 0.f ? 0.f : 1.f / l;  // no key seen: zero; a NaN stays
-        unsigned char* tile = sm + t * SM::kTileBytes;
-        const int r = threadIdx.x & 127;
-#pragma unroll
-        for (int x = 0; x < D; x += 32) {
-            float o[32];
-            if (steps > 0) {
-                tmem_ld32(tO[t] + lane0 + x, o);
-                tmem_wait_ld();
-            } else {
-#pragma unroll
-                for (int i = 0; i < 32; ++i) o[i] = 0.f;
-            }
-#pragma unroll
-            for (int i = 0; i < 32; ++i) o[i] *= inv;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) st_chunk16<true>(tile, r, x / 8 + i, o + 8 * i);
-        }
-        if (row < sq.lq)
-            p.lse[sq.q0 * p.lse_seq + h * p.lse_head + row] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
-        __syncwarp();
-        // each warp stores its 32 rows, D * 2 / 16 lanes a row
-        constexpr int CH = D / 8;
-        for (int i = lane; i < 32 * CH; i += 32) {
-            const int rr = 32 * (warp & 3) + i / CH, ch = i % CH;
-            const int grow = (2 * qb + t) * kTile + rr;
-            if (grow < sq.lq)
-                *reinterpret_cast<uint4*>(p.o + ((long long)(sq.q0 + grow) * p.Hq + h) * D + 8 * ch) =
-                    *reinterpret_cast<const uint4*>(tile + t16_off(rr, ch));
-        }
+        if (row < sq.lq && t < p.tiles)
+            p.lse[sq.q0 * p.lse_seq + h * p.lse_head + row] = l == 0.f ? -INFINITY : (m + __log2f(l)) * kLn2;
+        store_rows<D>(tO[t], inv, steps > 0, sm + t * SM::kTileBytes,
+                      p.o + ((long long)(sq.q0 + (qt + t) * kTile) * p.Hq + h) * D, (long long)p.Hq * D,
+                      t < p.tiles ? sq.lq - (qt + t) * kTile : 0);
     }
     tc_fence_before();
     __syncthreads();
@@ -420,8 +411,14 @@ cudaError_t run_fwd(const Problem& p, void* o, float* lse, cudaStream_t st) {
     a.Hq = p.Hq; a.Hk = p.Hk; a.causal = p.causal; a.window = p.window;
     for (int i = 0; i < p.n;) {
         long long blocks;
-        a.n = gather_seqs(p, i, false, 2 * kTile, a.seq, &i, &blocks);
+        const int first = i;
+        a.tiles = 2;
+        a.n = gather_seqs(p, first, false, 2 * kTile, a.seq, &i, &blocks);
         if (a.n == 0) continue;
+        if (blocks * p.Hq < kSMs) {
+            a.tiles = 1;
+            a.n = gather_seqs(p, first, false, kTile, a.seq, &i, &blocks);
+        }
         err = p.d == 128 ? launch<128>(a, (unsigned)(blocks * p.Hq), st) : launch<64>(a, (unsigned)(blocks * p.Hq), st);
         if (err != cudaSuccess) return err;
     }
