@@ -36,10 +36,10 @@ struct Problem {
     }
 };
 
-// Up to kMaxSeqs sequences from `first` on whose `rows` (queries or keys) number at least
-// one, the longest first, with their blocks of `rows_per_block` rows counted into block0.
-// Returns how many; `next` is where the following launch starts, `blocks` the total.
-int gather_seqs(const Problem& p, int first, bool by_keys, int rows_per_block, Seq* out, int* next,
+// Sequences [first, last) of the call (at most kMaxSeqs) whose `rows` (queries, or keys with
+// by_keys) number at least one, the longest first, with their blocks of rows_per_block rows
+// counted into block0.  Returns how many; `blocks`: the total.
+int gather_seqs(const Problem& p, int first, int last, bool by_keys, int rows_per_block, Seq* out,
                 long long* blocks);
 
 cudaError_t run_fwd(const Problem& p, void* o, float* lse, cudaStream_t st);

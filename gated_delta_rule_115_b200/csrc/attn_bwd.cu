@@ -5,14 +5,15 @@
 //     ds_ij = p_ij (dO_i . v_j - D_i),                D_i = dO_i . o_i
 //     dq_i  = scale sum_j ds_ij k_j,     dk_j = scale sum_i ds_ij q_i
 //
-// Three kernels: D; then dk and dv, a block owning 128 keys of one key head and walking the
-// queries of its group's heads; then dq, a block owning 128 queries and walking the keys.
+// D first; then two kinds of blocks: for dk and dv, a block owning 128 keys of one key head
+// and walking the queries of its group's heads; for dq, one owning 128 queries and walking
+// the keys.
 // Each sum is therefore formed by one block, in tensor memory, in a fixed order: no atomics,
 // no float32 gradient buffers, and shared key heads need no second pass.  The price is that
 // the scores and dO . v are formed twice (7 products a pair of tiles, where 5 would do if dq
 // were scattered).
 //
-// In both, tensor memory holds the scores of a step (S, 128 columns), dO . v (P, 128) and the
+// In both kinds, tensor memory holds the scores of a step (S, 128 columns), dO . v (P, 128) and the
 // sums.  Eight warps take a row and 64 of the 128 columns a thread, turn the scores into p and
 // the pair into ds, and write them, rounded to bf16 (half a step, 2^-8), over the columns of S
 // that they have read, where they are the A operand of the products that follow.
@@ -24,6 +25,8 @@
 //
 // Bound by the tensor cores (14 d flops a visible pair here) with the exponentials close
 // behind (2 a pair, 16 a clock and SM).
+#include <algorithm>
+
 #include "attn_dev.cuh"
 #include "profile.h"
 #include "tmap.h"
@@ -44,8 +47,9 @@ struct BwdParams {
     __nv_bfloat16 *dq, *dk, *dv;
     long long lse_seq, lse_head;
     float scale, scale_log2;
-    int Hq, Hk, causal, window, n;
-    Seq seq[kMaxSeqs];
+    int Hq, Hk, group, causal, window;
+    int kv_blocks, q_blocks, n_kv, n_q;
+    Seq kv[kMaxSeqs], q[kMaxSeqs];     // the sequences in blocks of keys, and of queries
 };
 
 // ------------------------------------------------------------------ D = dO . o
@@ -148,18 +152,16 @@ struct DkvBars {
 // (as one whole of 128 columns, each step waited for its own scores and its own exponentials
 // in turn: 3400 clocks a step, of which the tensor cores ran 2550).
 template <int D>
-__global__ void __launch_bounds__(kThreads, 1) k_attn_dkv(const __grid_constant__ BwdParams p) {
+__device__ __forceinline__ void dkv_block(const BwdParams& p, unsigned char* sm, int blk, int hk) {
     using SM = DkvSmem<D>;
     constexpr int NS = SM::kStages;
-    extern __shared__ __align__(1024) unsigned char sm[];
     DkvBars<NS>* bar = reinterpret_cast<DkvBars<NS>*>(sm + SM::kBars);
     static_assert(sizeof(DkvBars<NS>) <= SM::kBytes - SM::kBars, "barriers");
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int blk = blockIdx.x / p.Hk, hk = blockIdx.x % p.Hk;
-    const Seq sq = p.seq[find_seq(p.seq, p.n, blk)];
+    const Seq sq = p.kv[find_seq(p.kv, p.n_kv, blk)];
     const int kb = blk - sq.block0;  // with a causal mask the first keys are seen most
-    const int G = p.Hq / p.Hk;
+    const int G = p.group;
     const int off = sq.lk - sq.lq;
     const int k0 = kb * kTile;
 
@@ -172,7 +174,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_dkv(const __grid_constant_
     }
     const int per = max(0, hi - lo), steps = per * G;
 
-    if (threadIdx.x == 0) {
+    // The loading warp sets the barriers up and sends the resident tiles off before the block
+    // meets: they take longer than everything else that comes before the first product.
+    if (threadIdx.x == 32 * 11) {
         mbar_init(&bar->res_full, 1);
         for (int i = 0; i < NS; ++i) {
             mbar_init(bar->full + i, 2);
@@ -189,6 +193,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_dkv(const __grid_constant_
         }
         mbar_init(&bar->final_done, 1);
         fence_barrier_init();
+        if (steps > 0) {
+            mbar_arrive_expect_tx(&bar->res_full, 2 * SM::kTileBytes);
+            load_tile<D>(sm, &p.tk, hk, sq.k0 + k0, &bar->res_full);
+            load_tile<D>(sm + SM::kTileBytes, &p.tv, hk, sq.k0 + k0, &bar->res_full);
+        }
     }
     if (warp == 8) tmem_alloc(&bar->tmem_slot, 512);
     tc_fence_before();
@@ -202,13 +211,14 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_dkv(const __grid_constant_
         // ---------------------------------------------------------------- loads
         bool ok = true;
         uint32_t tails = 0;
-        if (lane == 0 && steps > 0) {
-            mbar_arrive_expect_tx(&bar->res_full, 2 * SM::kTileBytes);
-            load_tile<D>(sm, &p.tk, hk, sq.k0 + k0, &bar->res_full);
-            load_tile<D>(sm + SM::kTileBytes, &p.tv, hk, sq.k0 + k0, &bar->res_full);
-        }
+        int tile = 0, head = 0;  // of step i
         for (int i = 0; i < steps && ok; ++i) {
-            const int st = i % NS, h = hk * G + i / per, i0 = (lo + i % per) * kTile;
+            const int st = i % NS, i0 = (lo + tile) * kTile;
+            const int h = hk * G + head;
+            if (++tile == per) {
+                tile = 0;
+                ++head;
+            }
             if (i >= NS) ok = warp_wait(bar->empty + st, (i / NS - 1) & 1);
             if (!ok) break;
             ok = load_pair<D>(sm + SM::kRing + st * 2 * SM::kTileBytes, &p.tq, &p.tdo, h, sq.q0 + i0, sq.lq - i0,
@@ -307,12 +317,14 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_dkv(const __grid_constant_
         const int key = k0 + (threadIdx.x & 127);  // the thread's row
         const float c = p.scale_log2;
         bool ok = true;
+        int tile = 0;  // of step j
         for (int j = 0; j < steps && ok; ++j) {
             const uint32_t x = tmem + lane0 + 128u * wg + (uint32_t)(j & 1) * 64u;
             const uint32_t y = tmem + lane0 + 128u * wg + (uint32_t)(1 - (j & 1)) * 64u;
             const float4* nl = reinterpret_cast<const float4*>(vec + (j % NS) * 2 * kTile + 64 * wg);
             const float4* dl = nl + kTile / 4;
-            const int i0 = (lo + j % per) * kTile;
+            const int i0 = (lo + tile) * kTile;
+            if (++tile == per) tile = 0;
             // visible columns [a, b) of the thread's 64
             int a = 0, b = 64;
             const bool mask = (p.causal && i0 + off < k0 + kTile - 1) || (p.window && i0 + kTile - 1 + off - p.window >= k0);
@@ -427,19 +439,16 @@ struct DqBars {
 // alternate between two places, so that a step's are formed while the step before is still
 // at its exponentials.
 template <int D>
-__global__ void __launch_bounds__(kThreads, 1) k_attn_dq(const __grid_constant__ BwdParams p) {
+__device__ __forceinline__ void dq_block(const BwdParams& p, unsigned char* sm, int blk, int h, int hk) {
     using SM = DqSmem<D>;
     constexpr int NK = SM::kKeys, NV = SM::kVals;
-    extern __shared__ __align__(1024) unsigned char sm[];
     DqBars<NK, NV>* bar = reinterpret_cast<DqBars<NK, NV>*>(sm + SM::kBars);
     static_assert(sizeof(DqBars<NK, NV>) <= SM::kBytes - SM::kBars, "barriers");
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int blk = blockIdx.x / p.Hq, h = blockIdx.x % p.Hq;
-    const Seq sq = p.seq[find_seq(p.seq, p.n, blk)];
+    const Seq sq = p.q[find_seq(p.q, p.n_q, blk)];
     const int nblk = (sq.lq + kTile - 1) / kTile;
     const int qb = nblk - 1 - (blk - sq.block0);
-    const int hk = h / (p.Hq / p.Hk);
     const int off = sq.lk - sq.lq;
     const int r0 = qb * kTile, r1 = min(r0 + kTile, sq.lq) - 1;
 
@@ -449,7 +458,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_dq(const __grid_constant__
     const int lo = first / kTile;
     const int steps = last < first ? 0 : last / kTile + 1 - lo;
 
-    if (threadIdx.x == 0) {
+    if (threadIdx.x == 32 * 11) {  // as above
         mbar_init(&bar->res_full, 1);
         for (int i = 0; i < NK; ++i) {
             mbar_init(bar->k_full + i, 1);
@@ -469,6 +478,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_dq(const __grid_constant__
         mbar_init(&bar->dp_read, 8);
         mbar_init(&bar->final_done, 1);
         fence_barrier_init();
+        if (steps > 0) {
+            mbar_arrive_expect_tx(&bar->res_full, 2 * SM::kTileBytes);
+            load_tile<D>(sm, &p.tq, h, sq.q0 + r0, &bar->res_full);
+            load_tile<D>(sm + SM::kTileBytes, &p.tdo, h, sq.q0 + r0, &bar->res_full);
+        }
     }
     if (warp == 8) tmem_alloc(&bar->tmem_slot, 512);
     tc_fence_before();
@@ -480,11 +494,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_dq(const __grid_constant__
     if (warp == 11) {
         // ---------------------------------------------------------------- loads
         bool ok = true;
-        if (lane == 0 && steps > 0) {
-            mbar_arrive_expect_tx(&bar->res_full, 2 * SM::kTileBytes);
-            load_tile<D>(sm, &p.tq, h, sq.q0 + r0, &bar->res_full);
-            load_tile<D>(sm + SM::kTileBytes, &p.tdo, h, sq.q0 + r0, &bar->res_full);
-        }
         for (int i = 0; i < steps && ok; ++i) {
             const int j0 = (lo + i) * kTile, rows = sq.lk - j0;
             const int ks = i % NK, vs = i % NV;
@@ -643,11 +652,26 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_dq(const __grid_constant__
     }
 }
 
+// The blocks of dk and dv, then those of dq, in one launch: the second kind fills the SMs
+// that the first leaves idle at its end.  Grid (key head, block): kv_blocks blocks of keys,
+// then a block of queries for each head of the group in turn.
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1) k_attn_bwd(const __grid_constant__ BwdParams p) {
+    extern __shared__ __align__(1024) unsigned char sm[];
+    const int blk = block_index(), hk = blockIdx.x;
+    if (blk < p.kv_blocks) {
+        dkv_block<D>(p, sm, blk, hk);
+    } else {
+        const unsigned i = (unsigned)(blk - p.kv_blocks), qblk = i / (unsigned)p.group;
+        if ((int)qblk < p.q_blocks) dq_block<D>(p, sm, (int)qblk, hk * p.group + (int)(i - qblk * p.group), hk);
+    }
+}
+
 template <int D>
 cudaError_t run(const Problem& p, BwdParams& a, const void* o, const void* dO, float* delta, cudaStream_t st) {
-    static std::atomic<uint64_t> done_kv{0}, done_q{0};
-    cudaError_t err = allow_smem(k_attn_dkv<D>, DkvSmem<D>::kBytes, done_kv);
-    if (err == cudaSuccess) err = allow_smem(k_attn_dq<D>, DqSmem<D>::kBytes, done_q);
+    constexpr int kSmem = DkvSmem<D>::kBytes > DqSmem<D>::kBytes ? DkvSmem<D>::kBytes : DqSmem<D>::kBytes;
+    static std::atomic<uint64_t> done{0};
+    cudaError_t err = allow_smem(k_attn_bwd<D>, kSmem, done);
     if (err != cudaSuccess) return err;
     if (p.q_rows > 0) {
         const long long rows = p.q_rows * p.Hq;
@@ -658,19 +682,16 @@ cudaError_t run(const Problem& p, BwdParams& a, const void* o, const void* dO, f
                        p.Hq, p.Tq, p.lse_seq, p.lse_head));
         if ((err = cudaGetLastError()) != cudaSuccess) return err;
     }
-    long long blocks;
-    for (int i = 0; i < p.n;) {
-        a.n = gather_seqs(p, i, true, kTile, a.seq, &i, &blocks);
-        if (a.n == 0) continue;
-        MUIR_TIMED("k_attn_dkv", st,
-                   k_attn_dkv<D><<<(unsigned)(blocks * p.Hk), kThreads, DkvSmem<D>::kBytes, st>>>(a));
-        if ((err = cudaGetLastError()) != cudaSuccess) return err;
-    }
-    for (int i = 0; i < p.n;) {
-        a.n = gather_seqs(p, i, false, kTile, a.seq, &i, &blocks);
-        if (a.n == 0) continue;
-        MUIR_TIMED("k_attn_dq", st,
-                   k_attn_dq<D><<<(unsigned)(blocks * p.Hq), kThreads, DqSmem<D>::kBytes, st>>>(a));
+    for (int i = 0; i < p.n; i += kMaxSeqs) {
+        const int last = std::min(i + kMaxSeqs, p.n);
+        long long kv_blocks, q_blocks;
+        a.n_kv = gather_seqs(p, i, last, true, kTile, a.kv, &kv_blocks);
+        a.n_q = gather_seqs(p, i, last, false, kTile, a.q, &q_blocks);
+        a.kv_blocks = (int)kv_blocks;
+        a.q_blocks = (int)q_blocks;
+        const long long blocks = kv_blocks + q_blocks * a.group;
+        if (blocks == 0) continue;
+        MUIR_TIMED("k_attn_bwd", st, k_attn_bwd<D><<<block_grid(p.Hk, blocks), kThreads, kSmem, st>>>(a));
         if ((err = cudaGetLastError()) != cudaSuccess) return err;
     }
     return cudaSuccess;
@@ -703,7 +724,7 @@ cudaError_t run_bwd(const Problem& p, const void* o, const float* lse, const voi
     a.lse_head = p.lse_head;
     a.scale = p.scale;
     a.scale_log2 = p.scale * kLog2e;
-    a.Hq = p.Hq; a.Hk = p.Hk; a.causal = p.causal; a.window = p.window;
+    a.Hq = p.Hq; a.Hk = p.Hk; a.group = p.Hq / p.Hk; a.causal = p.causal; a.window = p.window;
     return p.d == 128 ? run<128>(p, a, o, dO, static_cast<float*>(ws), st)
                       : run<64>(p, a, o, dO, static_cast<float*>(ws), st);
 }

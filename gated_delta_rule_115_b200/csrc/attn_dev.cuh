@@ -171,6 +171,19 @@ __device__ __forceinline__ void store_rows(uint32_t tsrc, float f, bool any, uns
     }
 }
 
+// Blocks of a launch lie on the grid as (head, block % 65535, block / 65535): no division
+// before a block's first load.
+constexpr unsigned kGridY = 65535;
+inline dim3 block_grid(int heads, long long blocks) {
+    return dim3((unsigned)heads, (unsigned)(blocks < kGridY ? blocks : kGridY),
+                (unsigned)((blocks + kGridY - 1) / kGridY));
+}
+__device__ __forceinline__ int block_index() { return (int)(blockIdx.y + kGridY * blockIdx.z); }
+
+// Key head of query head h < 2^16: h / group, by the reciprocal (off by under 2^-22 h / group,
+// where half a head's distance to the next integer is 1 / (2 group)).
+__device__ __forceinline__ int key_head(int h, float inv_group) { return (int)(((float)h + 0.5f) * inv_group); }
+
 // The sequence that block `i` belongs to (block0 ascending, the first 0).
 __device__ __forceinline__ int find_seq(const Seq* s, int n, int i) {
     int lo = 0, hi = n - 1;

@@ -48,7 +48,8 @@ struct FwdParams {
     float* lse;
     long long lse_seq, lse_head;
     float scale_log2;
-    int Hq, Hk, causal, window, tiles, n;  // tiles: query tiles of a block
+    float inv_group;                       // Hk / Hq
+    int Hq, causal, window, tiles, blocks, n;  // tiles: query tiles of a block
     Seq seq[kMaxSeqs];
 };
 
@@ -77,12 +78,14 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fwd(const __grid_constant_
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tail_bar + 1);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int blk = blockIdx.x / p.Hq, h = blockIdx.x % p.Hq;
+    const int blk = block_index(), h = blockIdx.x;
+    if (blk >= p.blocks) return;
     const Seq sq = p.seq[find_seq(p.seq, p.n, blk)];
     // the longest rows of a causal sequence first
-    const int nblk = (sq.lq + p.tiles * kTile - 1) / (p.tiles * kTile);
+    const int nblk = (sq.lq + p.tiles * kTile - 1) >> (p.tiles == 2 ? 8 : 7);
+    static_assert(kTile == 128, "shift");
     const int qt = (nblk - 1 - (blk - sq.block0)) * p.tiles;  // its first query tile
-    const int hk = h / (p.Hq / p.Hk);
+    const int hk = key_head(h, p.inv_group);
     const int off = sq.lk - sq.lq;
 
     // key tiles [lo, hi) of each of the two query tiles
@@ -365,24 +368,23 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fwd(const __grid_constant_
 }
 
 template <int D>
-cudaError_t launch(const FwdParams& a, unsigned blocks, cudaStream_t st) {
+cudaError_t launch(const FwdParams& a, cudaStream_t st) {
     static std::atomic<uint64_t> done{0};
     const cudaError_t err = allow_smem(k_attn_fwd<D>, FwdSmem<D>::kBytes, done);
     if (err != cudaSuccess) return err;
-    MUIR_TIMED("k_attn_fwd", st, k_attn_fwd<D><<<blocks, kThreads, FwdSmem<D>::kBytes, st>>>(a));
+    MUIR_TIMED("k_attn_fwd", st, k_attn_fwd<D><<<block_grid(a.Hq, a.blocks), kThreads, FwdSmem<D>::kBytes, st>>>(a));
     return cudaGetLastError();
 }
 
 }  // namespace
 
-int gather_seqs(const Problem& p, int first, bool by_keys, int rows_per_block, Seq* out, int* next,
+int gather_seqs(const Problem& p, int first, int last, bool by_keys, int rows_per_block, Seq* out,
                 long long* blocks) {
-    int n = 0, i = first;
-    for (; i < p.n && n < kMaxSeqs; ++i) {
+    int n = 0;
+    for (int i = first; i < last; ++i) {
         const Seq s = p.seq(i);
         if ((by_keys ? s.lk : s.lq) > 0) out[n++] = s;
     }
-    *next = i;
     std::sort(out, out + n, [by_keys](const Seq& x, const Seq& y) {
         const int lx = by_keys ? x.lk : x.lq, ly = by_keys ? y.lk : y.lq;
         return lx != ly ? lx > ly : x.q0 < y.q0;
@@ -408,18 +410,21 @@ cudaError_t run_fwd(const Problem& p, void* o, float* lse, cudaStream_t st) {
     a.lse_seq = p.lse_seq;
     a.lse_head = p.lse_head;
     a.scale_log2 = p.scale * kLog2e;
-    a.Hq = p.Hq; a.Hk = p.Hk; a.causal = p.causal; a.window = p.window;
-    for (int i = 0; i < p.n;) {
+    a.Hq = p.Hq; a.inv_group = (float)p.Hk / (float)p.Hq; a.causal = p.causal; a.window = p.window;
+    for (int i = 0; i < p.n; i += kMaxSeqs) {
         long long blocks;
-        const int first = i;
+        const int last = std::min(i + kMaxSeqs, p.n);
         a.tiles = 2;
-        a.n = gather_seqs(p, first, false, 2 * kTile, a.seq, &i, &blocks);
+        a.n = gather_seqs(p, i, last, false, 2 * kTile, a.seq, &blocks);
         if (a.n == 0) continue;
+        // One tile a block where two leave SMs without a block: 256 tokens of 2 heads of 128
+        // 11.6 -> 8.3 us, 1024 tokens 21.2 -> 16.8.
         if (blocks * p.Hq < kSMs) {
             a.tiles = 1;
-            a.n = gather_seqs(p, first, false, kTile, a.seq, &i, &blocks);
+            a.n = gather_seqs(p, i, last, false, kTile, a.seq, &blocks);
         }
-        err = p.d == 128 ? launch<128>(a, (unsigned)(blocks * p.Hq), st) : launch<64>(a, (unsigned)(blocks * p.Hq), st);
+        a.blocks = (int)blocks;
+        err = p.d == 128 ? launch<128>(a, st) : launch<64>(a, st);
         if (err != cudaSuccess) return err;
     }
     return cudaSuccess;
