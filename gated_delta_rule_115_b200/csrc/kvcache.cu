@@ -164,6 +164,7 @@ constexpr int kStepStages = 3;
 constexpr int kGroups = kStepKeys / 16;    // groups of 16 keys, within one page each
 constexpr int kU = kWarpKeys / 16;         // a warp's
 constexpr int kMaxRows = 16;               // query heads of a block
+constexpr int kMaxSplits = 128;            // of a sequence; two to a thread of the smallest join
 constexpr float kSlack = 8.f;              // log2 of how far a weight may exceed 1
 constexpr float kWeightExp = 7.f;          // fp16 weights are 2^(score - reference + 7) <= 2^15
 
@@ -601,20 +602,25 @@ __global__ void __launch_bounds__(kStepThreads, HT == 1 ? 2 : 1) k_attn_step(con
     }
 }
 
-// Splits of a sequence and head together: weights 2^(lse_i - max).
+// Splits of a sequence and head together: weights 2^(lse_i - max), in the order of the splits.
+// (Joined inside a cluster through shared memory instead, 4097 tokens of one stream took as
+// long, and batches waited for whole clusters of free SMs: 106 -> 137 us at 64 streams.)
 template <int D>
 __global__ void __launch_bounds__(D) k_attn_step_join(const float* part, const float* lse, __nv_bfloat16* o,
                                                       int splits) {
+    __shared__ float w[kMaxSplits];
     const long long head = blockIdx.x;
     const int ch = threadIdx.x;
+    if (ch < splits) w[ch] = lse[head * splits + ch];
+    if (ch + D < splits) w[ch + D] = lse[head * splits + ch + D];
+    __syncthreads();
     float mx = -INFINITY;
-    for (int i = 0; i < splits; ++i) mx = fmaxf(mx, lse[head * splits + i]);
+    for (int i = 0; i < splits; ++i) mx = fmaxf(mx, w[i]);
     const float ms = mx == -INFINITY ? 0.f : mx;
     float sum = 0.f, a = 0.f;
-    for (int i = 0; i < splits; ++i) {
-        const float e = lse[head * splits + i];
-        if (e == -INFINITY) continue;
-        const float f = ex2(e - ms);
+#pragma unroll 8
+    for (int i = 0; i < splits; ++i) {  // a split without visible keys: weight 0, o = 0
+        const float f = ex2(w[i] - ms);
         sum += f;
         a += f * part[(head * splits + i) * D + ch];
     }
@@ -647,14 +653,17 @@ int attn_step_splits(int B, int Hq, int Hk, int page, int max_pages) {
     const int per = step_heads(Hq, Hk);
     const long long units = (long long)B * Hk * ((Hq / Hk + per - 1) / per);
     const long long cap = (long long)page * max_pages;
-    // enough blocks for the resident ones of 148 SMs, and none longer than 2048 keys, so
-    // that one long sequence of a ragged batch does not run on after the others
-    long long s = (2 * 148 + units - 1) / units;
+    // As many blocks as are resident on 148 SMs, two each (one more starts a second round: 2
+    // streams of 8192 tokens and 8 key heads 15.7 us at 19 splits, 12.3 at 16), and none longer
+    // than 2048 keys, so that one long sequence of a ragged batch does not run on after the
+    // others, nor shorter than 256, where a block is mostly its start (4097 tokens of one
+    // stream, 4 key heads: 7.8 us at 256 keys, 8.9 at 512).
+    long long s = 2 * 148 / units;
     const long long by_len = (cap + 2047) / 2048;
     if (s < by_len) s = by_len;
     const long long most = (cap + 255) / 256;
     if (s > most) s = most;
-    if (s > 128) s = 128;
+    if (s > kMaxSplits) s = kMaxSplits;
     return s < 1 ? 1 : (int)s;
 }
 
