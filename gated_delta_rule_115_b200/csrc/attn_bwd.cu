@@ -422,22 +422,24 @@ struct DqSmem {
     static constexpr int kK = 2 * kTileBytes;                          // after the two resident tiles
     static constexpr int kV = kK + kKeys * kTileBytes;
     static constexpr int kBars = kV + kVals * kTileBytes;
-    static constexpr int kBytes = kBars + 256;
+    static constexpr int kBytes = kBars + 512;
 };
 
 template <int NK, int NV>
 struct DqBars {
     uint64_t res_full;
     uint64_t k_full[NK], k_empty[NK], v_full[NV], v_empty[NV], tail;
-    uint64_t s_full[2], dp_full;       // products of a step in tensor memory (S of even, odd steps)
-    uint64_t dp_read, ds_full[2];      // eight warps: P read, ds written
-    uint64_t acc_done[2], final_done;  // a step's last product, the last step's
+    // of each half of the columns, S, ds and the last product of even and of odd steps:
+    uint64_t s_full[4], dp_full[2];    // products of a step in tensor memory
+    uint64_t dp_read[2], ds_full[4];   // four warps: P read, ds written
+    uint64_t acc_done[4];
+    uint64_t final_done;
     uint32_t tmem_slot;
 };
 
-// dq of 128 queries of one head: rows of the products are queries, columns keys.  The scores
-// alternate between two places, so that a step's are formed while the step before is still
-// at its exponentials.
+// dq of 128 queries of one head: rows of the products are queries, columns keys, in two halves
+// that go their own ways as above.  The scores alternate between two places, so that a step's
+// are formed while the step before is still at its exponentials.
 template <int D>
 __device__ __forceinline__ void dq_block(const BwdParams& p, unsigned char* sm, int blk, int h, int hk) {
     using SM = DqSmem<D>;
@@ -469,13 +471,15 @@ __device__ __forceinline__ void dq_block(const BwdParams& p, unsigned char* sm, 
             mbar_init(bar->v_empty + i, 1);
         }
         mbar_init(&bar->tail, 1);
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < 4; ++i) {
             mbar_init(bar->s_full + i, 1);
-            mbar_init(bar->ds_full + i, 8);
+            mbar_init(bar->ds_full + i, 4);
             mbar_init(bar->acc_done + i, 1);
         }
-        mbar_init(&bar->dp_full, 1);
-        mbar_init(&bar->dp_read, 8);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(bar->dp_full + i, 1);
+            mbar_init(bar->dp_read + i, 4);
+        }
         mbar_init(&bar->final_done, 1);
         fence_barrier_init();
         if (steps > 0) {
@@ -525,7 +529,7 @@ __device__ __forceinline__ void dq_block(const BwdParams& p, unsigned char* sm, 
         if (!ok && lane == 0) atomicOr(&g_bwd_timeouts, 8u);
     } else if (warp >= 8) {
         // ---------------------------------------------------------------- products
-        constexpr uint32_t id_s = idesc(kBF16, 128, 128, false, false);
+        constexpr uint32_t id_s = idesc(kBF16, 128, 64, false, false);
         constexpr uint32_t id_a = idesc(kBF16, 128, D, false, true);
         bool ok = true;
         if (lane != 0 || steps == 0) {
@@ -533,42 +537,54 @@ __device__ __forceinline__ void dq_block(const BwdParams& p, unsigned char* sm, 
             ok = mbar_wait(&bar->res_full, 0);
             const uint32_t a = saddr(sm);
             for (int j = 0; j < steps && ok; ++j) {
-                ok = mbar_wait(bar->k_full + j % NK, (j / NK) & 1) &&
-                     (j < 2 || mbar_wait(bar->acc_done + (j & 1), ((j - 2) >> 1) & 1));
-                if (!ok) break;
-                tc_fence_after();
                 const uint32_t b = saddr(sm + SM::kK + (j % NK) * SM::kTileBytes);
-                const uint32_t d = tmem + (uint32_t)(j & 1) * 128u;
+                ok = mbar_wait(bar->k_full + j % NK, (j / NK) & 1);
 #pragma unroll
-                for (int k = 0; k < D; k += 16) mma_f16(d, kdesc16(a, 0, k), kdesc16(b, 0, k), id_s, k ? 1u : 0u);
-                mma_commit(bar->s_full + (j & 1));
+                for (int u = 0; u < 2; ++u) {
+                    ok = ok && (j < 2 || mbar_wait(bar->acc_done + 2 * u + (j & 1), ((j - 2) >> 1) & 1));
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint32_t d = tmem + (uint32_t)(j & 1) * 128u + 64u * u;
+#pragma unroll
+                    for (int k = 0; k < D; k += 16)
+                        mma_f16(d, kdesc16(a, 0, k), kdesc16(b, 64 * u, k), id_s, k ? 1u : 0u);
+                    mma_commit(bar->s_full + 2 * u + (j & 1));
+                }
             }
         } else if (warp == 9) {  // P = dO V^T
             ok = mbar_wait(&bar->res_full, 0);
             const uint32_t a = saddr(sm + SM::kTileBytes);
             for (int j = 0; j < steps && ok; ++j) {
-                ok = mbar_wait(bar->v_full + j % NV, (j / NV) & 1) && (j == 0 || mbar_wait(&bar->dp_read, (j - 1) & 1));
-                if (!ok) break;
-                tc_fence_after();
                 const uint32_t b = saddr(sm + SM::kV + (j % NV) * SM::kTileBytes);
+                ok = mbar_wait(bar->v_full + j % NV, (j / NV) & 1);
 #pragma unroll
-                for (int k = 0; k < D; k += 16) mma_f16(tP, kdesc16(a, 0, k), kdesc16(b, 0, k), id_s, k ? 1u : 0u);
-                if (j + NV < steps) mma_commit(bar->v_empty + j % NV);
-                mma_commit(&bar->dp_full);
+                for (int u = 0; u < 2; ++u) {
+                    ok = ok && (j == 0 || mbar_wait(bar->dp_read + u, (j - 1) & 1));
+                    if (!ok) break;
+                    tc_fence_after();
+#pragma unroll
+                    for (int k = 0; k < D; k += 16)
+                        mma_f16(tP + 64u * u, kdesc16(a, 0, k), kdesc16(b, 64 * u, k), id_s, k ? 1u : 0u);
+                    if (u == 1 && j + NV < steps) mma_commit(bar->v_empty + j % NV);
+                    mma_commit(bar->dp_full + u);
+                }
             }
         } else {  // dq += ds K
             for (int j = 0; j < steps && ok; ++j) {
-                ok = mbar_wait(bar->ds_full + (j & 1), (j >> 1) & 1);
-                if (!ok) break;
-                tc_fence_after();
-                const uint32_t x = tmem + (uint32_t)(j & 1) * 128u;
                 const uint32_t b = saddr(sm + SM::kK + (j % NK) * SM::kTileBytes);
 #pragma unroll
-                for (int k = 0; k < kTile; k += 16)  // ds: columns 0-31 of each half of S
-                    mma_f16_ta(tQ, x + (k & 64) + (k & 63) / 2, mdesc16(b, k, 0), id_a, (j || k) ? 1u : 0u);
-                if (j + NK < steps) mma_commit(bar->k_empty + j % NK);
-                if (j + 2 < steps) mma_commit(bar->acc_done + (j & 1));
-                if (j + 1 == steps) mma_commit(&bar->final_done);
+                for (int u = 0; u < 2; ++u) {
+                    ok = ok && mbar_wait(bar->ds_full + 2 * u + (j & 1), (j >> 1) & 1);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint32_t x = tmem + (uint32_t)(j & 1) * 128u + 64u * u;
+#pragma unroll
+                    for (int k = 0; k < 64; k += 16)  // ds: the first 32 columns of S
+                        mma_f16_ta(tQ, x + k / 2, mdesc16(b, 64 * u + k, 0), id_a, (j || u || k) ? 1u : 0u);
+                    if (u == 1 && j + NK < steps) mma_commit(bar->k_empty + j % NK);
+                    if (j + 2 < steps) mma_commit(bar->acc_done + 2 * u + (j & 1));
+                }
+                if (ok && j + 1 == steps) mma_commit(&bar->final_done);
             }
         }
         if (!ok) atomicOr(&g_bwd_timeouts, 16u);
@@ -596,7 +612,7 @@ __device__ __forceinline__ void dq_block(const BwdParams& p, unsigned char* sm, 
             const int j0 = (lo + j) * kTile;
             const bool mask = j0 + kTile - 1 > all_max || j0 < all_min;
             const int a = kmin - j0 - 64 * wg, b = kmax - j0 - 64 * wg;
-            ok = warp_wait(bar->s_full + (j & 1), (j >> 1) & 1);
+            ok = warp_wait(bar->s_full + 2 * wg + (j & 1), (j >> 1) & 1);
             if (!ok) break;
             tc_fence_after();
             float s[2][32];
@@ -605,7 +621,7 @@ __device__ __forceinline__ void dq_block(const BwdParams& p, unsigned char* sm, 
             tmem_wait_ld();
 #pragma unroll
             for (int i = 0; i < 64; ++i) s[i >> 5][i & 31] = ex2(fmaf(s[i >> 5][i & 31], c, nl));
-            ok = warp_wait(&bar->dp_full, j & 1);
+            ok = warp_wait(bar->dp_full + wg, j & 1);
             if (!ok) break;
             tc_fence_after();
             uint32_t w[32];
@@ -617,7 +633,7 @@ __device__ __forceinline__ void dq_block(const BwdParams& p, unsigned char* sm, 
                 if (hlf) {
                     tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(&bar->dp_read);
+                    if (lane == 0) mbar_arrive(bar->dp_read + wg);
                 }
 #pragma unroll
                 for (int i = 0; i < 32; ++i) s[hlf][i] *= dp[i] - dl;
@@ -632,7 +648,7 @@ __device__ __forceinline__ void dq_block(const BwdParams& p, unsigned char* sm, 
             tmem_wait_st();
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(bar->ds_full + (j & 1));
+            if (lane == 0) mbar_arrive(bar->ds_full + 2 * wg + (j & 1));
         }
         if (steps > 0 && ok) {
             ok = warp_wait(&bar->final_done, 0);
