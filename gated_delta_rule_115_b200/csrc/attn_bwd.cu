@@ -325,14 +325,11 @@ __device__ __forceinline__ void dkv_block(const BwdParams& p, unsigned char* sm,
             const float4* dl = nl + kTile / 4;
             const int i0 = (lo + tile) * kTile;
             if (++tile == per) tile = 0;
-            // visible columns [a, b) of the thread's 64
-            int a = 0, b = 64;
-            const bool mask = (p.causal && i0 + off < k0 + kTile - 1) || (p.window && i0 + kTile - 1 + off - p.window >= k0);
-            if (mask) {
-                const int first = key - off - i0 - 64 * wg;
-                if (p.causal) a = first;
-                if (p.window) b = min(b, first + p.window);
-            }
+            // the first of the thread's 64 columns that sees its key, and whether some column
+            // of the tile does not (causal), or no longer does (window)
+            const int sees = key - off - i0 - 64 * wg;
+            const bool before = p.causal && i0 + off < k0 + kTile - 1;
+            const bool behind = p.window && i0 + kTile - 1 + off - p.window >= k0;
             ok = warp_wait(bar->s_full + wg, j & 1) && warp_wait(bar->full + j % NS, (j / NS) & 1);
             if (!ok) break;
             tc_fence_after();
@@ -340,6 +337,14 @@ __device__ __forceinline__ void dkv_block(const BwdParams& p, unsigned char* sm,
             tmem_ld32(x, s[0]);
             tmem_ld32(x + 32, s[1]);
             tmem_wait_ld();
+            if (before) {
+#pragma unroll
+                for (int i = 0; i < 64; ++i) s[i >> 5][i & 31] = i >= sees ? s[i >> 5][i & 31] : -INFINITY;
+            }
+            if (behind) {
+#pragma unroll
+                for (int i = 0; i < 64; ++i) s[i >> 5][i & 31] = i < sees + p.window ? s[i >> 5][i & 31] : -INFINITY;
+            }
             uint32_t w[32];
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
@@ -349,10 +354,6 @@ __device__ __forceinline__ void dkv_block(const BwdParams& p, unsigned char* sm,
                 v[1] = ex2(fmaf(v[1], c, n.y));
                 v[2] = ex2(fmaf(v[2], c, n.z));
                 v[3] = ex2(fmaf(v[3], c, n.w));
-            }
-            if (mask) {
-#pragma unroll
-                for (int i = 0; i < 64; ++i) s[i >> 5][i & 31] = (i >= a && i < b) ? s[i >> 5][i & 31] : 0.f;
             }
 #pragma unroll
             for (int i = 0; i < 32; ++i) w[i] = bf16x2(s[i >> 4][(2 * i) & 31], s[i >> 4][(2 * i + 1) & 31]);
@@ -383,10 +384,6 @@ __device__ __forceinline__ void dkv_block(const BwdParams& p, unsigned char* sm,
                     v[1] *= dp[4 * i + 1] - n.y;
                     v[2] *= dp[4 * i + 2] - n.z;
                     v[3] *= dp[4 * i + 3] - n.w;
-                }
-                if (mask) {  // zero weight times whatever stood there
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) s[hlf][i] = (32 * hlf + i >= a && 32 * hlf + i < b) ? s[hlf][i] : 0.f;
                 }
 #pragma unroll
                 for (int i = 0; i < 16; ++i) w[16 * hlf + i] = bf16x2(s[hlf][2 * i], s[hlf][2 * i + 1]);
@@ -470,7 +467,7 @@ __device__ __forceinline__ void dq_block(const BwdParams& p, unsigned char* sm, 
             mbar_init(bar->v_full + i, 1);
             mbar_init(bar->v_empty + i, 1);
         }
-        mbar_init(&bar->tail, 1);
+        mbar_init(&bar->tail, 2);
         for (int i = 0; i < 4; ++i) {
             mbar_init(bar->s_full + i, 1);
             mbar_init(bar->ds_full + i, 4);
@@ -503,10 +500,11 @@ __device__ __forceinline__ void dq_block(const BwdParams& p, unsigned char* sm, 
             const int ks = i % NK, vs = i % NV;
             if (i >= NK) ok = warp_wait(bar->k_empty + ks, (i / NK - 1) & 1);
             if (!ok) break;
-            // key rows behind the sequence's end: their ds is zero, which a NaN or an
-            // infinity there would survive (the value rows' dots are discarded instead)
-            unsigned char* kd = sm + SM::kK + ks * SM::kTileBytes;
-            uint64_t* kb = rows < kTile ? &bar->tail : bar->k_full + ks;
+            // Rows behind the sequence's end: their p and ds are zero, which a NaN or an
+            // infinity there would survive.
+            unsigned char *kd = sm + SM::kK + ks * SM::kTileBytes, *vd = sm + SM::kV + vs * SM::kTileBytes;
+            const bool tail = rows < kTile;
+            uint64_t *kb = tail ? &bar->tail : bar->k_full + ks, *vb = tail ? &bar->tail : bar->v_full + vs;
             if (lane == 0) {
                 mbar_arrive_expect_tx(kb, SM::kTileBytes);
                 load_tile<D>(kd, &p.tk, hk, sq.k0 + j0, kb);
@@ -515,15 +513,19 @@ __device__ __forceinline__ void dq_block(const BwdParams& p, unsigned char* sm, 
             if (i >= NV) ok = warp_wait(bar->v_empty + vs, (i / NV - 1) & 1);
             if (!ok) break;
             if (lane == 0) {
-                mbar_arrive_expect_tx(bar->v_full + vs, SM::kTileBytes);
-                load_tile<D>(sm + SM::kV + vs * SM::kTileBytes, &p.tv, hk, sq.k0 + j0, bar->v_full + vs);
+                mbar_arrive_expect_tx(vb, SM::kTileBytes);
+                load_tile<D>(vd, &p.tv, hk, sq.k0 + j0, vb);
             }
             __syncwarp();
-            if (rows < kTile) {
+            if (tail) {
                 ok = warp_wait(&bar->tail, 0);
                 if (!ok) break;
                 zero_rows<D>(kd, rows);
-                if (lane == 0) mbar_arrive(bar->k_full + ks);
+                zero_rows<D>(vd, rows);
+                if (lane == 0) {
+                    mbar_arrive(bar->k_full + ks);
+                    mbar_arrive(bar->v_full + vs);
+                }
             }
         }
         if (!ok && lane == 0) atomicOr(&g_bwd_timeouts, 8u);
@@ -610,8 +612,7 @@ __device__ __forceinline__ void dq_block(const BwdParams& p, unsigned char* sm, 
         for (int j = 0; j < steps && ok; ++j) {
             const uint32_t x = tmem + lane0 + (uint32_t)(j & 1) * 128u + 64u * wg;
             const int j0 = (lo + j) * kTile;
-            const bool mask = j0 + kTile - 1 > all_max || j0 < all_min;
-            const int a = kmin - j0 - 64 * wg, b = kmax - j0 - 64 * wg;
+            const int a = kmin - j0 - 64 * wg, b = kmax - j0 - 64 * wg;  // visible columns [a, b] of the 64
             ok = warp_wait(bar->s_full + 2 * wg + (j & 1), (j >> 1) & 1);
             if (!ok) break;
             tc_fence_after();
@@ -619,6 +620,14 @@ __device__ __forceinline__ void dq_block(const BwdParams& p, unsigned char* sm, 
             tmem_ld32(x, s[0]);
             tmem_ld32(x + 32, s[1]);
             tmem_wait_ld();
+            if (j0 + kTile - 1 > all_max) {
+#pragma unroll
+                for (int i = 0; i < 64; ++i) s[i >> 5][i & 31] = i <= b ? s[i >> 5][i & 31] : -INFINITY;
+            }
+            if (j0 < all_min) {
+#pragma unroll
+                for (int i = 0; i < 64; ++i) s[i >> 5][i & 31] = i >= a ? s[i >> 5][i & 31] : -INFINITY;
+            }
 #pragma unroll
             for (int i = 0; i < 64; ++i) s[i >> 5][i & 31] = ex2(fmaf(s[i >> 5][i & 31], c, nl));
             ok = warp_wait(bar->dp_full + wg, j & 1);
@@ -637,10 +646,6 @@ __device__ __forceinline__ void dq_block(const BwdParams& p, unsigned char* sm, 
                 }
 #pragma unroll
                 for (int i = 0; i < 32; ++i) s[hlf][i] *= dp[i] - dl;
-                if (mask) {
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) s[hlf][i] = (32 * hlf + i >= a && 32 * hlf + i <= b) ? s[hlf][i] : 0.f;
-                }
 #pragma unroll
                 for (int i = 0; i < 16; ++i) w[16 * hlf + i] = bf16x2(s[hlf][2 * i], s[hlf][2 * i + 1]);
             }
