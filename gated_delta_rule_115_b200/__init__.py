@@ -536,6 +536,8 @@ def _rows(t, name, dev=None):
         st = sb if B > 1 else H * d
     elif B > 1 and sb != T * st:
         raise ValueError(f"{name}: tokens must be evenly spaced")
+    if st < H * d:
+        raise ValueError(f"{name}: tokens must not overlap (expanded tensors are not taken)")
     return t.data_ptr(), st
 
 

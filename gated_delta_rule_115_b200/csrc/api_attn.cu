@@ -31,6 +31,8 @@ muir_status check_attn(const muir_attn_shape* s) {
     // rows are int32 (with room for a tile past the end), blocks of 128 rows and heads a grid
     if ((long long)s->B * s->Tq > 0x7fff0000LL || (long long)s->B * s->Tk > 0x7fff0000LL || s->Hq > 65536)
         return MUIR_ERR_UNSUPPORTED;
+    // a query's position less the window, and a key's plus it, stay in int32
+    if (s->Tq + 2LL * s->Tk > 0x7fffffffLL) return MUIR_ERR_UNSUPPORTED;
     const long long tq = (s->Tq + 127LL) / 128, tk = (s->Tk + 127LL) / 128;
     if ((s->B * tq + 65536) * s->Hq > 0x7fffffffLL || (s->B * tk + 65536) * s->Hk > 0x7fffffffLL)
         return MUIR_ERR_UNSUPPORTED;
@@ -56,7 +58,8 @@ muir::attn::Problem attn_problem(const muir_attn_shape* s, const void* q, const 
                                  int n, const long long* cu_q, const long long* cu_k) {
     muir::attn::Problem p;
     p.Hq = s->Hq; p.Hk = s->Hk; p.d = s->d;
-    p.causal = s->causal != 0; p.window = s->window; p.scale = s->scale;
+    p.causal = s->causal != 0; p.scale = s->scale;
+    p.window = s->window < s->Tk ? s->window : 0;  // one that hides nothing is none
     p.q_ld = s->q_ld ? s->q_ld : (long long)s->Hq * s->d;
     p.k_ld = s->k_ld ? s->k_ld : (long long)s->Hk * s->d;
     p.v_ld = s->v_ld ? s->v_ld : (long long)s->Hk * s->d;

@@ -28,7 +28,6 @@ __device__ unsigned int g_kv_timeouts;
 
 namespace {
 
-constexpr int kAppThreads = 256;
 
 __device__ __forceinline__ void kv_unpack(const uint4& a, float* v, float) {
     v[0] = __uint_as_float(a.x); v[1] = __uint_as_float(a.y);
@@ -43,9 +42,30 @@ __device__ __forceinline__ void kv_unpack(const uint4& a, float* v, __nv_bfloat1
     }
 }
 
-// Two floats -> two e4m3 codes (round to nearest even, saturating; NaN stays NaN).
-__device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
-    return (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E4M3);
+// Four floats -> four e4m3 codes (round to nearest even, saturating; NaN stays NaN).
+__device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
+    uint32_t r;
+    asm("{\n.reg .b16 lo, hi;\ncvt.rn.satfinite.e4m3x2.f32 lo, %2, %1;\n"
+        "cvt.rn.satfinite.e4m3x2.f32 hi, %4, %3;\nmov.b32 %0, {lo, hi};\n}"
+        : "=r"(r)
+        : "f"(a), "f"(b), "f"(c), "f"(d));
+    return r;
+}
+
+// Running maximum of magnitudes, NaN passed over; infinities count.
+__device__ __forceinline__ uint32_t bf16x2_max(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+__device__ __forceinline__ float vec_amax(const uint4& x, float amax, float) {
+    amax = fmaxf(fmaxf(amax, fabsf(__uint_as_float(x.x))), fabsf(__uint_as_float(x.y)));
+    return fmaxf(fmaxf(amax, fabsf(__uint_as_float(x.z))), fabsf(__uint_as_float(x.w)));
+}
+__device__ __forceinline__ float vec_amax(const uint4& x, float amax, __nv_bfloat16) {
+    constexpr uint32_t kAbs = 0x7fff7fffu;
+    const uint32_t m = bf16x2_max(bf16x2_max(x.x & kAbs, x.y & kAbs), bf16x2_max(x.z & kAbs, x.w & kAbs));
+    return fmaxf(fmaxf(amax, __uint_as_float(m << 16)), __uint_as_float(m & 0xffff0000u));
 }
 __device__ __forceinline__ float2 from_e4m3x2(uint32_t two) {
     const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)two, __NV_E4M3);
@@ -55,23 +75,38 @@ __device__ __forceinline__ float2 from_e4m3x2(uint32_t two) {
 // Smallest power of two s >= 2^kMinScaleExp with amax <= 448 s (448 = 0.875 2^9).
 constexpr int kMinScaleExp = -100;
 __device__ __forceinline__ float scale_for(float amax) {
-    int e;
-    const float m = frexpf(amax, &e);  // amax = m 2^e, m in [0.5, 1); amax = 0: m = e = 0
-    e -= m <= 0.875f ? 9 : 8;
-    if (amax == 0.f || e < kMinScaleExp) e = kMinScaleExp;
-    return ldexpf(1.f, e);
+    const uint32_t u = __float_as_uint(amax);
+    // amax = 1.f 2^x: 2^(x-8) reaches 448 = 1.75 2^8 while 1.f <= 1.75, then the next
+    int e = (int)(u >> 23) - 127 - ((u & 0x7fffffu) <= 0x600000u ? 8 : 7);
+    if (e < kMinScaleExp) e = kMinScaleExp;  // zero and subnormal magnitudes too
+    return __uint_as_float((uint32_t)(e + 127) << 23);
+}
+
+// Largest of the block's values, which every thread gets.
+template <int NT>
+__device__ __forceinline__ float block_max(float v, float* part) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < NT / 32; ++w) v = fmaxf(v, part[w]);
+    return v;
 }
 
 // One block per (page a sequence's new tokens touch, head, keys or values): the new
 // rows' largest finite magnitude, the page's scale, held rows encoded again if the
 // scale grew, new rows encoded.  Rows of the page behind the new tokens stay as they are.
 // The rows are read once, NV vectors of 16 bytes a thread, all in flight together, and
-// wait in registers for the scale (read twice through a loop instead, 27000 tokens of 4
-// heads of 128 took 15 us where this takes 11).
-template <typename T, int D, int NV>
-__global__ void __launch_bounds__(kAppThreads) k_kv_append(AppendArgs p) {
-    constexpr int V = 16 / (int)sizeof(T);  // channels per vector
+// wait in registers for the scale.  Bound by issue slots next to HBM: magnitudes are
+// compared two bfloat16 at a time (one by one, with addresses formed for every vector, it
+// took 18 instructions a value and 16.2 us for 17800 tokens of 4 heads of 128, where this takes
+// 10.7: 5.1 TB/s).
+template <typename T, int D, int NT, int NV>
+__global__ void __launch_bounds__(NT) k_kv_append(AppendArgs p) {
+    constexpr int V = 16 / (int)sizeof(T);       // channels per vector
     constexpr int PER_ROW = D / V;
+    constexpr int STEP = NT / PER_ROW;  // rows between a thread's vectors
     const int b = blockIdx.z >> 1, which = blockIdx.z & 1, h = blockIdx.y;
     const int start = p.start[b];
     int count = p.count ? p.count[b] : p.T;
@@ -85,70 +120,66 @@ __global__ void __launch_bounds__(kAppThreads) k_kv_append(AppendArgs p) {
     if (lo >= hi || slot >= p.max_pages) return;
     const int id = p.table[(long long)b * p.max_pages + slot];
 
+    const int row = threadIdx.x / PER_ROW, col = (threadIdx.x % PER_ROW) * V;  // the thread's first vector
     const long long ld = which ? p.v_ld : p.k_ld;
-    const T* src = static_cast<const T*>(which ? p.v : p.k) + ((long long)b * p.T + lo) * ld + (long long)h * D;
-    const int items = (hi - lo) * PER_ROW;
+    const T* src = static_cast<const T*>(which ? p.v : p.k) + ((long long)b * p.T + lo + row) * ld + (long long)h * D + col;
     uint4 x[NV];
 #pragma unroll
     for (int n = 0; n < NV; ++n) {
-        const int i = n * kAppThreads + (int)threadIdx.x;
         x[n] = make_uint4(0u, 0u, 0u, 0u);
-        if (i < items) x[n] = *reinterpret_cast<const uint4*>(src + (i / PER_ROW) * ld + (i % PER_ROW) * V);
+        if (row + n * STEP < hi - lo) x[n] = *reinterpret_cast<const uint4*>(src + n * STEP * ld);
     }
     if (id < 0 || id >= p.num_pages) return;  // the whole block
-    unsigned char* dst = static_cast<unsigned char*>(which ? p.v_pages : p.k_pages) +
-                         ((long long)id * p.Hk + h) * p.page * D;
+    unsigned char* page = static_cast<unsigned char*>(which ? p.v_pages : p.k_pages) +
+                          ((long long)id * p.Hk + h) * p.page * D;
     float* scale = (which ? p.v_scale : p.k_scale) + (long long)id * p.Hk + h;
     const int held = (int)(start + lo - page0);  // rows of the page before the new ones
     const float old = held > 0 ? *scale : 0.f;
 
+    __shared__ float part[2][NT / 32];
     float amax = 0.f;
 #pragma unroll
-    for (int n = 0; n < NV; ++n) {
-        float v[V];
-        kv_unpack(x[n], v, T());
+    for (int n = 0; n < NV; ++n) amax = vec_amax(x[n], amax, T());
+    amax = block_max<NT>(amax, part[0]);  // and every thread has read the old scale
+    if (amax > 3.402823466e38f) {     // an infinity among them: the largest finite one instead
+        amax = 0.f;
 #pragma unroll
-        for (int j = 0; j < V; ++j) {
-            const float a = fabsf(v[j]);
-            if (a <= 3.402823466e38f) amax = fmaxf(amax, a);  // false for infinities and NaN
+        for (int n = 0; n < NV; ++n) {
+            float v[V];
+            kv_unpack(x[n], v, T());
+#pragma unroll
+            for (int j = 0; j < V; ++j)
+                if (fabsf(v[j]) <= 3.402823466e38f) amax = fmaxf(amax, fabsf(v[j]));
         }
+        amax = block_max<NT>(amax, part[1]);
     }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-    __shared__ float part[kAppThreads / 32];
-    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = amax;
-    __syncthreads();  // also: every thread has read the old scale
-#pragma unroll
-    for (int w = 0; w < kAppThreads / 32; ++w) amax = fmaxf(amax, part[w]);
     const float now = fmaxf(old, scale_for(amax));
     if (threadIdx.x == 0) *scale = now;
 
-    const float inv = 1.f / now;  // exact: a power of two in [2^-120, 2^100]
+    const float inv = __frcp_rn(now);  // exact: a power of two in [2^-120, 2^100]
     if (old > 0.f && now != old) {
         const float ratio = old / now;
-        for (int i = threadIdx.x; i < held * (D / 4); i += kAppThreads) {
-            uint32_t* w = reinterpret_cast<uint32_t*>(dst) + i;
+        for (int i = threadIdx.x; i < held * (D / 4); i += NT) {
+            uint32_t* w = reinterpret_cast<uint32_t*>(page) + i;
             const uint32_t y = *w;
             const float2 a = from_e4m3x2(y & 0xffffu), c = from_e4m3x2(y >> 16);
-            *w = e4m3x2(a.x * ratio, a.y * ratio) | (e4m3x2(c.x * ratio, c.y * ratio) << 16);
+            *w = e4m3x4(a.x * ratio, a.y * ratio, c.x * ratio, c.y * ratio);
         }
     }
+    unsigned char* dst = page + (held + row) * D + col;
 #pragma unroll
     for (int n = 0; n < NV; ++n) {
-        const int i = n * kAppThreads + (int)threadIdx.x;
-        if (i >= items) break;
+        if (row + n * STEP >= hi - lo) break;
         float v[V];
         kv_unpack(x[n], v, T());
         uint32_t w[V / 4];
 #pragma unroll
         for (int j = 0; j < V / 4; ++j)
-            w[j] = e4m3x2(v[4 * j] * inv, v[4 * j + 1] * inv) |
-                   (e4m3x2(v[4 * j + 2] * inv, v[4 * j + 3] * inv) << 16);
-        uint32_t* o = reinterpret_cast<uint32_t*>(dst + (long long)(held + i / PER_ROW) * D + (i % PER_ROW) * V);
+            w[j] = e4m3x4(v[4 * j] * inv, v[4 * j + 1] * inv, v[4 * j + 2] * inv, v[4 * j + 3] * inv);
         if (V == 8)
-            *reinterpret_cast<uint2*>(o) = make_uint2(w[0], w[V / 4 - 1]);
+            *reinterpret_cast<uint2*>(dst + n * STEP * D) = make_uint2(w[0], w[V / 4 - 1]);
         else
-            *o = w[0];
+            *reinterpret_cast<uint32_t*>(dst + n * STEP * D) = w[0];
     }
 }
 
@@ -631,12 +662,14 @@ __global__ void __launch_bounds__(D) k_attn_step_join(const float* part, const f
 
 template <typename T, int D>
 static cudaError_t append(const AppendArgs& a, dim3 grid, cudaStream_t st) {
-    // vectors a thread holds of the most rows that one page takes in this call
+    // The most rows that one page takes in this call, in vectors a thread.  Fewer threads with
+    // more vectors each form fewer addresses and scales: 128 with 8 rather than 256 with 4:
+    // 17800 tokens of 4 heads of 128, 12.9 -> 10.7 us.
     const int rows = a.T < a.page ? a.T : a.page;
-    const int nv = (rows * D * (int)sizeof(T) / 16 + kAppThreads - 1) / kAppThreads;
-    if (nv <= 1) MUIR_TIMED("k_kv_append", st, k_kv_append<T, D, 1><<<grid, kAppThreads, 0, st>>>(a));
-    else if (nv <= 4) MUIR_TIMED("k_kv_append", st, k_kv_append<T, D, 4><<<grid, kAppThreads, 0, st>>>(a));
-    else MUIR_TIMED("k_kv_append", st, k_kv_append<T, D, 16><<<grid, kAppThreads, 0, st>>>(a));
+    const int vecs = rows * D * (int)sizeof(T) / 16;
+    if (vecs <= 128) MUIR_TIMED("k_kv_append", st, k_kv_append<T, D, 128, 1><<<grid, 128, 0, st>>>(a));
+    else if (vecs <= 128 * 8) MUIR_TIMED("k_kv_append", st, k_kv_append<T, D, 128, 8><<<grid, 128, 0, st>>>(a));
+    else MUIR_TIMED("k_kv_append", st, k_kv_append<T, D, 256, 16><<<grid, 256, 0, st>>>(a));
     return cudaGetLastError();
 }
 

@@ -166,7 +166,7 @@ def attn(m, backward=False, **over):
     (dict(window=-1), INVALID), (dict(scale=0.0), INVALID), (dict(scale=-1.0), INVALID),
     (dict(scale=math.nan), INVALID), (dict(scale=math.inf), INVALID), (dict(d=96), UNSUPPORTED),
     (dict(d=256), UNSUPPORTED), (dict(q_ld=64), INVALID), (dict(k_ld=132), INVALID), (dict(v_ld=-128), INVALID),
-    (dict(B=1 << 16, Tq=1 << 16), UNSUPPORTED), (dict(B=1 << 20, Tq=1, Hq=1 << 16, Hk=1), UNSUPPORTED),
+    (dict(B=1 << 16, Tq=1 << 16), UNSUPPORTED), (dict(Tk=1 << 30), UNSUPPORTED), (dict(B=1 << 20, Tq=1, Hq=1 << 16, Hk=1), UNSUPPORTED),
     (dict(q=None), INVALID), (dict(k=FAKE + 8), INVALID), (dict(v=None), INVALID), (dict(o=None), INVALID),
     (dict(lse=None), INVALID), (dict(lse=FAKE + 2), INVALID)])
 def test_attention_refusals(m, over, code):
