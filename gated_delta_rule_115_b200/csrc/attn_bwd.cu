@@ -39,6 +39,7 @@ __device__ unsigned int g_bwd_timeouts;
 namespace {
 
 constexpr int kThreads = 384;
+constexpr int kSMs = 148;
 constexpr float kLog2e = 1.4426950408889634f;
 
 struct BwdParams {
@@ -48,6 +49,7 @@ struct BwdParams {
     long long lse_seq, lse_head;
     float scale, scale_log2;
     int Hq, Hk, group, causal, window;
+    int dq_heads;                      // query heads of a block of dq: 1, or (d = 64) 2 of a group
     int kv_blocks, q_blocks, n_kv, n_q;
     Seq kv[kMaxSeqs], q[kMaxSeqs];     // the sequences in blocks of keys, and of queries
 };
@@ -416,7 +418,8 @@ template <int D>
 struct DqSmem {
     static constexpr int kTileBytes = kTile * D * 2;
     static constexpr int kKeys = D == 128 ? 3 : 4, kVals = D == 128 ? 2 : 4;  // tiles of each ring
-    static constexpr int kK = 2 * kTileBytes;                          // after the two resident tiles
+    static constexpr int kHeads = D == 128 ? 1 : 2;                    // most heads of a block
+    static constexpr int kK = 2 * kHeads * kTileBytes;                 // after the resident tiles
     static constexpr int kV = kK + kKeys * kTileBytes;
     static constexpr int kBars = kV + kVals * kTileBytes;
     static constexpr int kBytes = kBars + 512;
@@ -437,8 +440,13 @@ struct DqBars {
 // dq of 128 queries of one head: rows of the products are queries, columns keys, in two halves
 // that go their own ways as above.  The scores alternate between two places, so that a step's
 // are formed while the step before is still at its exponentials.
+//
+// At D = 64 there is room for the tiles and the sums of two heads: a block of two heads of a
+// group takes each key tile for the one and then for the other, and its start and its end,
+// which cost as much as four steps, serve both.
 template <int D>
 __device__ __forceinline__ void dq_block(const BwdParams& p, unsigned char* sm, int blk, int h, int hk) {
+    const int sh = DqSmem<D>::kHeads == 1 ? 0 : p.dq_heads - 1;  // heads 1 << sh: h and h + sh
     using SM = DqSmem<D>;
     constexpr int NK = SM::kKeys, NV = SM::kVals;
     DqBars<NK, NV>* bar = reinterpret_cast<DqBars<NK, NV>*>(sm + SM::kBars);
@@ -455,7 +463,8 @@ __device__ __forceinline__ void dq_block(const BwdParams& p, unsigned char* sm, 
     if (p.causal) last = min(last, r1 + off);
     if (p.window) first = max(first, r0 + off - p.window + 1);
     const int lo = first / kTile;
-    const int steps = last < first ? 0 : last / kTile + 1 - lo;
+    const int tiles = last < first ? 0 : last / kTile + 1 - lo;
+    const int steps = tiles << sh;  // step i: key tile i >> sh, head h + (i & sh)
 
     if (threadIdx.x == 32 * 11) {  // as above
         mbar_init(&bar->res_full, 1);
@@ -480,9 +489,11 @@ __device__ __forceinline__ void dq_block(const BwdParams& p, unsigned char* sm, 
         mbar_init(&bar->final_done, 1);
         fence_barrier_init();
         if (steps > 0) {
-            mbar_arrive_expect_tx(&bar->res_full, 2 * SM::kTileBytes);
-            load_tile<D>(sm, &p.tq, h, sq.q0 + r0, &bar->res_full);
-            load_tile<D>(sm + SM::kTileBytes, &p.tdo, h, sq.q0 + r0, &bar->res_full);
+            mbar_arrive_expect_tx(&bar->res_full, (2 * SM::kTileBytes) << sh);
+            for (int n = 0; n <= sh; ++n) {
+                load_tile<D>(sm + 2 * n * SM::kTileBytes, &p.tq, h + n, sq.q0 + r0, &bar->res_full);
+                load_tile<D>(sm + (2 * n + 1) * SM::kTileBytes, &p.tdo, h + n, sq.q0 + r0, &bar->res_full);
+            }
         }
     }
     if (warp == 8) tmem_alloc(&bar->tmem_slot, 512);
@@ -495,7 +506,7 @@ __device__ __forceinline__ void dq_block(const BwdParams& p, unsigned char* sm, 
     if (warp == 11) {
         // ---------------------------------------------------------------- loads
         bool ok = true;
-        for (int i = 0; i < steps && ok; ++i) {
+        for (int i = 0; i < tiles && ok; ++i) {
             const int j0 = (lo + i) * kTile, rows = sq.lk - j0;
             const int ks = i % NK, vs = i % NV;
             if (i >= NK) ok = warp_wait(bar->k_empty + ks, (i / NK - 1) & 1);
@@ -537,56 +548,60 @@ __device__ __forceinline__ void dq_block(const BwdParams& p, unsigned char* sm, 
         if (lane != 0 || steps == 0) {
         } else if (warp == 8) {  // S = Q K^T, where the ds of two steps before was
             ok = mbar_wait(&bar->res_full, 0);
-            const uint32_t a = saddr(sm);
-            for (int j = 0; j < steps && ok; ++j) {
+            for (int i = 0; i < steps && ok; ++i) {
+                const int j = i >> sh;
+                const uint32_t a = saddr(sm + 2 * (i & sh) * SM::kTileBytes);
                 const uint32_t b = saddr(sm + SM::kK + (j % NK) * SM::kTileBytes);
                 ok = mbar_wait(bar->k_full + j % NK, (j / NK) & 1);
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
-                    ok = ok && (j < 2 || mbar_wait(bar->acc_done + 2 * u + (j & 1), ((j - 2) >> 1) & 1));
+                    ok = ok && (i < 2 || mbar_wait(bar->acc_done + 2 * u + (i & 1), ((i - 2) >> 1) & 1));
                     if (!ok) break;
                     tc_fence_after();
-                    const uint32_t d = tmem + (uint32_t)(j & 1) * 128u + 64u * u;
+                    const uint32_t d = tmem + (uint32_t)(i & 1) * 128u + 64u * u;
 #pragma unroll
                     for (int k = 0; k < D; k += 16)
                         mma_f16(d, kdesc16(a, 0, k), kdesc16(b, 64 * u, k), id_s, k ? 1u : 0u);
-                    mma_commit(bar->s_full + 2 * u + (j & 1));
+                    mma_commit(bar->s_full + 2 * u + (i & 1));
                 }
             }
         } else if (warp == 9) {  // P = dO V^T
             ok = mbar_wait(&bar->res_full, 0);
-            const uint32_t a = saddr(sm + SM::kTileBytes);
-            for (int j = 0; j < steps && ok; ++j) {
+            for (int i = 0; i < steps && ok; ++i) {
+                const int j = i >> sh;
+                const uint32_t a = saddr(sm + (2 * (i & sh) + 1) * SM::kTileBytes);
                 const uint32_t b = saddr(sm + SM::kV + (j % NV) * SM::kTileBytes);
                 ok = mbar_wait(bar->v_full + j % NV, (j / NV) & 1);
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
-                    ok = ok && (j == 0 || mbar_wait(bar->dp_read + u, (j - 1) & 1));
+                    ok = ok && (i == 0 || mbar_wait(bar->dp_read + u, (i - 1) & 1));
                     if (!ok) break;
                     tc_fence_after();
 #pragma unroll
                     for (int k = 0; k < D; k += 16)
                         mma_f16(tP + 64u * u, kdesc16(a, 0, k), kdesc16(b, 64 * u, k), id_s, k ? 1u : 0u);
-                    if (u == 1 && j + NV < steps) mma_commit(bar->v_empty + j % NV);
+                    if (u == 1 && (i & sh) == sh && j + NV < tiles) mma_commit(bar->v_empty + j % NV);
                     mma_commit(bar->dp_full + u);
                 }
             }
         } else {  // dq += ds K
-            for (int j = 0; j < steps && ok; ++j) {
+            for (int i = 0; i < steps && ok; ++i) {
+                const int j = i >> sh;
                 const uint32_t b = saddr(sm + SM::kK + (j % NK) * SM::kTileBytes);
+                const uint32_t d = tQ + (uint32_t)((i & sh) * D);
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
-                    ok = ok && mbar_wait(bar->ds_full + 2 * u + (j & 1), (j >> 1) & 1);
+                    ok = ok && mbar_wait(bar->ds_full + 2 * u + (i & 1), (i >> 1) & 1);
                     if (!ok) break;
                     tc_fence_after();
-                    const uint32_t x = tmem + (uint32_t)(j & 1) * 128u + 64u * u;
+                    const uint32_t x = tmem + (uint32_t)(i & 1) * 128u + 64u * u;
 #pragma unroll
                     for (int k = 0; k < 64; k += 16)  // ds: the first 32 columns of S
-                        mma_f16_ta(tQ, x + k / 2, mdesc16(b, 64 * u + k, 0), id_a, (j || u || k) ? 1u : 0u);
-                    if (u == 1 && j + NK < steps) mma_commit(bar->k_empty + j % NK);
-                    if (j + 2 < steps) mma_commit(bar->acc_done + 2 * u + (j & 1));
+                        mma_f16_ta(d, x + k / 2, mdesc16(b, 64 * u + k, 0), id_a, (j || u || k) ? 1u : 0u);
+                    if (u == 1 && (i & sh) == sh && j + NK < tiles) mma_commit(bar->k_empty + j % NK);
+                    if (i + 2 < steps) mma_commit(bar->acc_done + 2 * u + (i & 1));
                 }
-                if (ok && j + 1 == steps) mma_commit(&bar->final_done);
+                if (ok && i + 1 == steps) mma_commit(&bar->final_done);
             }
         }
         if (!ok) atomicOr(&g_bwd_timeouts, 16u);
@@ -600,18 +615,22 @@ __device__ __forceinline__ void dq_block(const BwdParams& p, unsigned char* sm, 
         const int kmin = p.window ? at - p.window + 1 : 0;
         const int all_max = p.causal ? min(sq.lk - 1, r0 + off) : sq.lk - 1;
         const int all_min = p.window ? r0 + kTile - 1 + off - p.window + 1 : 0;
-        float nl = -INFINITY, dl = 0.f;  // rows that do not exist and queries that see no key: no weight
-        if (row < sq.lq) {
-            const long long v = sq.q0 * p.lse_seq + h * p.lse_head + row;
-            const float e = p.lse[v];
-            if (e != -INFINITY) nl = -e * kLog2e;
-            dl = p.delta[v];
-        }
+        // rows that do not exist and queries that see no key: no weight
+        float nls[2] = {-INFINITY, -INFINITY}, dls[2] = {0.f, 0.f};
+#pragma unroll
+        for (int n = 0; n < SM::kHeads; ++n)
+            if (row < sq.lq && n <= sh) {
+                const long long v = sq.q0 * p.lse_seq + (h + n) * p.lse_head + row;
+                const float e = p.lse[v];
+                if (e != -INFINITY) nls[n] = -e * kLog2e;
+                dls[n] = p.delta[v];
+            }
         const float c = p.scale_log2;
         bool ok = true;
         for (int j = 0; j < steps && ok; ++j) {
             const uint32_t x = tmem + lane0 + (uint32_t)(j & 1) * 128u + 64u * wg;
-            const int j0 = (lo + j) * kTile;
+            const int j0 = (lo + (j >> sh)) * kTile;
+            const float nl = j & sh ? nls[1] : nls[0], dl = j & sh ? dls[1] : dls[0];
             const int a = kmin - j0 - 64 * wg, b = kmax - j0 - 64 * wg;  // visible columns [a, b] of the 64
             ok = warp_wait(bar->s_full + 2 * wg + (j & 1), (j >> 1) & 1);
             if (!ok) break;
@@ -661,8 +680,12 @@ __device__ __forceinline__ void dq_block(const BwdParams& p, unsigned char* sm, 
         }
         if (!ok && lane == 0) atomicOr(&g_bwd_timeouts, 32u);
         const long long ld = (long long)p.Hq * D;
-        if (wg == 0)
-            store_rows<D>(tQ, p.scale, steps > 0, sm, p.dq + (long long)(sq.q0 + r0) * ld + h * D, ld, sq.lq - r0);
+        __nv_bfloat16* dq = p.dq + (long long)(sq.q0 + r0) * ld + h * D;
+        unsigned char* tile = sm + wg * SM::kTileBytes;
+        if (sh)  // a head for each four warps
+            store_rows<D>(tQ + wg * D, p.scale, steps > 0, tile, dq + wg * D, ld, sq.lq - r0);
+        else     // half of the columns
+            store_rows<D / 2>(tQ + wg * (D / 2), p.scale, steps > 0, tile, dq + wg * (D / 2), ld, sq.lq - r0);
     }
     tc_fence_before();
     __syncthreads();
@@ -675,7 +698,7 @@ __device__ __forceinline__ void dq_block(const BwdParams& p, unsigned char* sm, 
 
 // The blocks of dk and dv, then those of dq, in one launch: the second kind fills the SMs
 // that the first leaves idle at its end.  Grid (key head, block): kv_blocks blocks of keys,
-// then a block of queries for each head of the group in turn.
+// then a block of queries for each dq_heads heads of the group in turn.
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1) k_attn_bwd(const __grid_constant__ BwdParams p) {
     extern __shared__ __align__(1024) unsigned char sm[];
@@ -683,8 +706,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_bwd(const __grid_constant_
     if (blk < p.kv_blocks) {
         dkv_block<D>(p, sm, blk, hk);
     } else {
-        const unsigned i = (unsigned)(blk - p.kv_blocks), qblk = i / (unsigned)p.group;
-        if ((int)qblk < p.q_blocks) dq_block<D>(p, sm, (int)qblk, hk * p.group + (int)(i - qblk * p.group), hk);
+        const unsigned i = (unsigned)(blk - p.kv_blocks), per = (unsigned)(p.group / p.dq_heads), qblk = i / per;
+        if ((int)qblk < p.q_blocks)
+            dq_block<D>(p, sm, (int)qblk, hk * p.group + (int)(i - qblk * per) * p.dq_heads, hk);
     }
 }
 
@@ -710,7 +734,11 @@ cudaError_t run(const Problem& p, BwdParams& a, const void* o, const void* dO, f
         a.n_q = gather_seqs(p, i, last, false, kTile, a.q, &q_blocks);
         a.kv_blocks = (int)kv_blocks;
         a.q_blocks = (int)q_blocks;
-        const long long blocks = kv_blocks + q_blocks * a.group;
+        // Two heads a block where the group is even, there is room, and the blocks still go
+        // round: packed windows of 5245 tokens, 16 heads over 4, 75.7 -> 71.1 us; 8 x 1024
+        // tokens 117.8 -> 113.0.
+        a.dq_heads = DqSmem<D>::kHeads == 2 && a.group % 2 == 0 && q_blocks * (p.Hq / 2) >= 2 * kSMs ? 2 : 1;
+        const long long blocks = kv_blocks + q_blocks * (a.group / a.dq_heads);
         if (blocks == 0) continue;
         MUIR_TIMED("k_attn_bwd", st, k_attn_bwd<D><<<block_grid(p.Hk, blocks), kThreads, kSmem, st>>>(a));
         if ((err = cudaGetLastError()) != cudaSuccess) return err;

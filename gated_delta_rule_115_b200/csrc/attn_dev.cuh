@@ -131,42 +131,46 @@ __device__ __forceinline__ void zero_rows(unsigned char* tile, int first) {
     __syncwarp();
 }
 
-// 128 lanes x D columns of tensor memory, each lane times its f, as bf16 rows of a token-major
-// tensor [rows][heads][D] (`ld` elements between rows, rows < `rows` only), through a tile of
+// 128 lanes x W columns of tensor memory, each lane times its f, as bf16 into columns of a
+// token-major tensor (`ld` elements between rows, rows < `rows` only), through a tile of
 // shared memory that nothing reads any more: a row is a lane in tensor memory, and a lane that
 // stored its own row would touch 32 lines with every store.  Four warps; `any` false: zeros.
-template <int D>
+template <int W>
 __device__ __forceinline__ void store_rows(uint32_t tsrc, float f, bool any, unsigned char* tile,
                                            __nv_bfloat16* dst, long long ld, int rows) {
     const int w = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31, r = 32 * w + lane;
     const uint32_t lane0 = (uint32_t)w << 21;
+    constexpr int N = W >= 64 ? 2 : 1;  // loads of 32 columns in flight
 #pragma unroll
-    for (int x = 0; x < D; x += 64) {
-        float v[2][32];
-        if (any) {
-            tmem_ld32(tsrc + lane0 + x, v[0]);
-            tmem_ld32(tsrc + lane0 + x + 32, v[1]);
-            tmem_wait_ld();
-        } else {
+    for (int x = 0; x < W; x += 32 * N) {
+        float v[N][32];
 #pragma unroll
-            for (int i = 0; i < 32; ++i) v[0][i] = v[1][i] = 0.f;
+        for (int n = 0; n < N; ++n) {
+            if (any) {
+                tmem_ld32(tsrc + lane0 + x + 32 * n, v[n]);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 32; ++i) v[n][i] = 0.f;
+            }
         }
+        if (any) tmem_wait_ld();
 #pragma unroll
-        for (int i = 0; i < 64; ++i) v[i >> 5][i & 31] *= f;
+        for (int i = 0; i < 32 * N; ++i) v[i >> 5][i & 31] *= f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) st_chunk16<true>(tile, r, x / 8 + i, v[i >> 2] + 8 * (i & 3));
+        for (int i = 0; i < 4 * N; ++i) st_chunk16<true>(tile, r, x / 8 + i, v[i >> 2] + 8 * (i & 3));
     }
     __syncwarp();
-    constexpr int CH = D / 8, RPI = 32 / CH;  // lanes a row, rows an instruction
+    constexpr int CH = W / 8, RPI = 32 / CH;  // lanes a row, rows an instruction
+    constexpr int U = 32 / RPI < 8 ? 32 / RPI : 8;
     const int rr0 = 32 * w + lane / CH, ch = lane % CH;
     __nv_bfloat16* out = dst + (long long)rr0 * ld + 8 * ch;
 #pragma unroll
-    for (int i = 0; i < 32 / RPI; i += 8) {
-        uint4 v[8];
+    for (int i = 0; i < 32 / RPI; i += U) {
+        uint4 v[U];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) v[k] = *reinterpret_cast<const uint4*>(tile + t16_off(rr0 + (i + k) * RPI, ch));
+        for (int k = 0; k < U; ++k) v[k] = *reinterpret_cast<const uint4*>(tile + t16_off(rr0 + (i + k) * RPI, ch));
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
+        for (int k = 0; k < U; ++k)
             if (rr0 + (i + k) * RPI < rows) *reinterpret_cast<uint4*>(out + (long long)(i + k) * RPI * ld) = v[k];
     }
 }

@@ -66,6 +66,10 @@ CASES = [
     (1, 640, 640, 2, 1, 64, True, 1), (1, 640, 640, 2, 1, 128, True, 128), (1, 700, 700, 2, 2, 64, True, 200),
     (2, 300, 500, 2, 1, 128, False, 150), (1, 1000, 1000, 6, 2, 128, True, 0), (1, 100, 1, 2, 2, 64, True, 0),
     (1, 385, 640, 1, 1, 128, False, 0), (3, 256, 256, 5, 1, 64, True, 77), (1, 2100, 2100, 1, 1, 128, True, 0),
+    # enough blocks for two query tiles each: of one head, or two heads' of an even group; the
+    # latter also has two heads to a block of dq at d = 64
+    (1, 1400, 1400, 28, 28, 128, True, 0), (1, 1400, 1400, 28, 28, 64, True, 300), (2, 900, 1000, 32, 2, 128, True, 0),
+    (1, 1201, 1201, 64, 2, 64, True, 0), (1, 1201, 700, 64, 2, 64, True, 111), (2, 640, 650, 64, 8, 64, False, 0),
 ]
 
 
