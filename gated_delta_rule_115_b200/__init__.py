@@ -1,8 +1,8 @@
 """Python binding of libmuir, the Muir gated delta rule on one NVIDIA B200.
 
-Argument marshalling only: every step of the computation runs in the CUDA
-kernels of ``libmuir.so`` (built in-tree by ``gated_delta_rule_115_b200.build``)
-behind the C ABI declared in ``include/muir.h``.  PyTorch supplies device
+Argument marshalling only (ctypes; a native module for the softmax-attention layer):
+every step of the computation runs in the CUDA kernels of ``libmuir.so`` (built in-tree
+by ``gated_delta_rule_115_b200.build``) behind the C ABI declared in ``include/muir.h``.  PyTorch supplies device
 memory and the current CUDA stream.  There is no CPU fallback: if the library
 is missing or a call fails, an exception is raised.
 
@@ -500,54 +500,24 @@ def qk_prologue_bwd(x, dy, out=None):
 # ------------------------------------------------------------------ softmax-attention layers
 
 
-# the current stream's handle and device, without building a Stream object for each call
-_raw_stream = torch._C._cuda_getCurrentRawStream
-_current_device = torch._C._cuda_getDevice
+_nat = None
 
 
-def _dev_call(name, t, *args):
-    """Calls ``name`` with the current stream of ``t``'s device, that device current."""
-    fn = getattr(_lib or lib(), name)
-    dev = t.device.index
-    if dev == _current_device():
-        rc = fn(*args, _raw_stream(dev))
-    else:
-        with torch.cuda.device(dev):
-            rc = fn(*args, _raw_stream(dev))
-    if rc != 0:
-        raise MuirError(name, rc)
-
-
-def _rows(t, name, dev=None):
-    """Address and token stride (0 = dense) of a ``[B, T, H, d]`` tensor whose heads are dense
-    within a token and whose tokens are evenly spaced (a part of a packed projection
-    qualifies)."""
-    if not t.is_cuda:
-        raise ValueError("libmuir takes CUDA tensors only")
-    if dev is not None and t.device != dev:
-        raise ValueError(f"{name} is on {t.device}, not on {dev}")
-    if t.is_contiguous():
-        return t.data_ptr(), 0
-    B, T, H, d = t.shape
-    sb, st, sh, sd = t.stride()
-    if (sd != 1 and d > 1) or (sh != d and H > 1):
-        raise ValueError(f"{name}: channels and heads of a token must be dense")
-    if T == 1:
-        st = sb if B > 1 else H * d
-    elif B > 1 and sb != T * st:
-        raise ValueError(f"{name}: tokens must be evenly spaced")
-    if st < H * d:
-        raise ValueError(f"{name}: tokens must not overlap (expanded tensors are not taken)")
-    return t.data_ptr(), st
-
-
-def _same(t, name, shape, dtype, dev):
-    """Address of a contiguous tensor of exactly this shape, type and device."""
-    if t is None:
-        return None
-    if t.shape != shape or t.dtype != dtype or t.device != dev or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {dev}")
-    return t.data_ptr()
+def _native():
+    """The native half of this binding (``_attn``, built from ``csrc/torch_binding.cpp``):
+    these operators are called once a token and layer, where ctypes marshalling would take
+    longer than the kernels."""
+    global _nat
+    if _nat is None:
+        lib()
+        try:
+            from . import _attn
+        except ImportError as e:
+            raise ImportError("the native binding is missing or was built for another torch: run "
+                              "`python -m gated_delta_rule_115_b200.build`") from e
+        _attn.load(LIB_PATH, MuirError)
+        _nat = _attn
+    return _nat
 
 
 def rotary_frequencies(rot, base=10000.0, scaling=None, factor=1.0, original_length=2048,
@@ -593,56 +563,7 @@ def rotary(q, k=None, positions=None, inv_freq=None, interleaved=False, mscale=1
     ``inverse`` applies the transpose, which maps an output gradient to the input's.
     ``q_out`` / ``k_out`` may be the inputs (in place).  Returns ``(q_out, k_out)``, or
     ``q_out`` alone without ``k``."""
-    B, T, Hq, d = q.shape
-    dev = q.device
-    dt = _dt(q)
-    if inv_freq is None:
-        raise ValueError("inv_freq is required (rotary_frequencies makes it)")
-    qp, ql = _rows(q, "q")
-    if q_out is None:
-        q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
-        op, ol = q_out.data_ptr(), 0
-    else:
-        if q_out.shape != q.shape or q_out.dtype != q.dtype:
-            raise ValueError("q_out must have q's shape and dtype")
-        op, ol = _rows(q_out, "q_out", dev)
-    Hk, kp, kl, kop, kol = 0, None, 0, None, 0
-    if k is not None:
-        if k.shape[:2] != q.shape[:2] or k.shape[3] != d or k.dtype != q.dtype:
-            raise ValueError("k must have q's batch, tokens, channels and dtype")
-        Hk = k.shape[2]
-        kp, kl = _rows(k, "k", dev)
-        if k_out is None:
-            k_out = torch.empty_like(k, memory_format=torch.contiguous_format)
-            kop, kol = k_out.data_ptr(), 0
-        else:
-            if k_out.shape != k.shape or k_out.dtype != k.dtype:
-                raise ValueError("k_out must have k's shape and dtype")
-            kop, kol = _rows(k_out, "k_out", dev)
-    elif k_out is not None:
-        raise ValueError("k_out without k")
-    rot = 2 * inv_freq.numel()
-    _dev_call("muir_rotary", q, B, T, Hq, Hk, d, rot, dt, qp, ql, kp, kl,
-              _same(positions, "positions", (B, T), torch.int32, dev),
-              _same(inv_freq, "inv_freq", (rot // 2,), torch.float64, dev), mscale,
-              int(bool(interleaved)), int(bool(inverse)), op, ol, kop, kol)
-    return q_out if k is None else (q_out, k_out)
-
-
-def _attn_shape(q, k, v, causal, window, scale):
-    """(MuirAttnShape, addresses of q, k, v)."""
-    B, Tq, Hq, d = q.shape
-    Bk, Tk, Hk, dk = k.shape
-    dev = q.device
-    if Bk != B or dk != d or v.shape != k.shape:
-        raise ValueError("q, k and v must agree in batch and channels, k and v in shape")
-    if q.dtype != torch.bfloat16 or k.dtype != torch.bfloat16 or v.dtype != torch.bfloat16:
-        raise TypeError("attention takes bfloat16 tensors")
-    qp, ql = _rows(q, "q")
-    kp, kl = _rows(k, "k", dev)
-    vp, vl = _rows(v, "v", dev)
-    return MuirAttnShape(B, Tq, Tk, Hq, Hk, d, 1 if causal else 0, window,
-                         d ** -0.5 if scale is None else scale, ql, kl, vl), qp, kp, vp
+    return (_nat or _native()).rotary(q, k, positions, inv_freq, interleaved, mscale, inverse, q_out, k_out)
 
 
 def attn_fwd(q, k, v, causal=True, window=0, scale=None):
@@ -651,64 +572,27 @@ def attn_fwd(q, k, v, causal=True, window=0, scale=None):
     stands at key position ``i + Tk - Tq``; ``causal`` hides later keys, ``window`` all but
     the last ``window``.  ``scale`` defaults to ``d ** -0.5``.  Returns ``(o, lse)`` with
     ``o [B, Tq, Hq, d]`` and float32 ``lse [B, Hq, Tq]``."""
-    s, qp, kp, vp = _attn_shape(q, k, v, causal, window, scale)
-    o = torch.empty(s.B, s.Tq, s.Hq, s.d, dtype=torch.bfloat16, device=q.device)
-    lse = torch.empty(s.B, s.Hq, s.Tq, dtype=torch.float32, device=q.device)
-    _dev_call("muir_attn_fwd", q, ctypes.byref(s), qp, kp, vp, o.data_ptr(), lse.data_ptr())
-    return o, lse
-
-
-def _attn_bwd(name, extra, q, k, v, o, lse, dO, causal, window, scale, ws):
-    s, qp, kp, vp = _attn_shape(q, k, v, causal, window, scale)
-    dev = q.device
-    shape = (s.B, s.Tq, s.Hq, s.d)
-    op = _same(o, "o", shape, torch.bfloat16, dev)
-    gp = _same(dO, "dO", shape, torch.bfloat16, dev)
-    lp = _same(lse, "lse", (s.B, s.Hq, s.Tq), torch.float32, dev)
-    grads = {"dq": torch.empty(shape, dtype=torch.bfloat16, device=dev)}
-    for n in ("dk", "dv"):
-        grads[n] = torch.empty(s.B, s.Tk, s.Hk, s.d, dtype=torch.bfloat16, device=dev)
-    wsb = _workspace(lib().muir_attn_bwd_workspace(ctypes.byref(s)), dev, ws)
-    _dev_call(name, q, ctypes.byref(s), *extra, qp, kp, vp, op, lp, gp, grads["dq"].data_ptr(),
-              grads["dk"].data_ptr(), grads["dv"].data_ptr(),
-              None if wsb is None else wsb.data_ptr(), 0 if wsb is None else wsb.numel())
-    return grads
+    return (_nat or _native()).attn_fwd(q, k, v, None, None, causal, window, scale)
 
 
 def attn_bwd(q, k, v, o, lse, dO, causal=True, window=0, scale=None, ws=None):
     """Gradients of ``sum(o * dO)`` (``muir_attn_bwd``) from :func:`attn_fwd`'s ``o`` and
     ``lse``; the probabilities are recomputed.  Returns a dict with ``dq, dk, dv``."""
-    return _attn_bwd("muir_attn_bwd", (), q, k, v, o, lse, dO, causal, window, scale, ws)
-
-
-def _cu_pair(cu_seqlens, cu_seqlens_k):
-    n, cu = _cu(cu_seqlens)
-    if cu_seqlens_k is None:
-        return n, cu, None
-    nk, ck = _cu(cu_seqlens_k)
-    if nk != n:
-        raise ValueError("cu_seqlens_k must have as many offsets as cu_seqlens")
-    return n, cu, ck
+    return (_nat or _native()).attn_bwd(q, k, v, o, lse, dO, None, None, causal, window, scale, ws)
 
 
 def attn_fwd_varlen(q, k, v, cu_seqlens, cu_seqlens_k=None, causal=True, window=0, scale=None):
     """:func:`attn_fwd` over packed sequences: ``q [1, T, Hq, d]``, ``k, v [1, Tk, Hk, d]`` with
     sequence i at rows ``cu_seqlens[i]:cu_seqlens[i+1]`` (a host list or CPU tensor;
     ``cu_seqlens_k`` for the keys where they differ).  ``lse`` is ``[1, Hq, T]``."""
-    n, cu, ck = _cu_pair(cu_seqlens, cu_seqlens_k)
-    s, qp, kp, vp = _attn_shape(q, k, v, causal, window, scale)
-    o = torch.empty(s.B, s.Tq, s.Hq, s.d, dtype=torch.bfloat16, device=q.device)
-    lse = torch.empty(s.B, s.Hq, s.Tq, dtype=torch.float32, device=q.device)
-    _dev_call("muir_attn_fwd_varlen", q, ctypes.byref(s), n, cu, ck, qp, kp, vp, o.data_ptr(),
-              lse.data_ptr())
-    return o, lse
+    return (_nat or _native()).attn_fwd(q, k, v, cu_seqlens, cu_seqlens_k, causal, window, scale)
 
 
 def attn_bwd_varlen(q, k, v, o, lse, dO, cu_seqlens, cu_seqlens_k=None, causal=True, window=0,
                     scale=None, ws=None):
     """Gradients through :func:`attn_fwd_varlen`; returns the dict of :func:`attn_bwd`."""
-    return _attn_bwd("muir_attn_bwd_varlen", _cu_pair(cu_seqlens, cu_seqlens_k), q, k, v, o, lse,
-                     dO, causal, window, scale, ws)
+    return (_nat or _native()).attn_bwd(q, k, v, o, lse, dO, cu_seqlens, cu_seqlens_k, causal, window,
+                                        scale, ws)
 
 
 def kv_cache(num_pages, Hk, page, d, device="cuda"):
@@ -719,38 +603,12 @@ def kv_cache(num_pages, Hk, page, d, device="cuda"):
     return z[0], z[1], *[torch.ones(num_pages, Hk, dtype=torch.float32, device=device) for _ in range(2)]
 
 
-def _cache(k_pages, v_pages, k_scale, v_scale, page_table, B, dev):
-    shape = k_pages.shape
-    num, Hk, page, d = shape
-    if page_table.dim() != 2 or page_table.shape[0] != B:
-        raise ValueError("page_table must be [B, max_pages]")
-    return MuirKvCache(
-        Hk, d, page, num, page_table.shape[1],
-        _same(k_pages, "k_pages", shape, torch.float8_e4m3fn, dev),
-        _same(v_pages, "v_pages", shape, torch.float8_e4m3fn, dev),
-        _same(k_scale, "k_scale", (num, Hk), torch.float32, dev),
-        _same(v_scale, "v_scale", (num, Hk), torch.float32, dev),
-        _same(page_table, "page_table", page_table.shape, torch.int32, dev))
-
-
 def kv_append(k, v, k_pages, v_pages, k_scale, v_scale, page_table, start, count=None):
     """Writes the tokens of ``k, v [B, T, Hk, d]`` (bfloat16 or float32) into the cache
     (:func:`kv_cache`), in place (``muir_kv_append``): token t of sequence b to position
     ``start[b] + t`` for t below ``count[b]`` (None: T).  ``page_table`` is int32
     ``[B, max_pages]``, ``start`` and ``count`` int32 ``[B]``, all on the device."""
-    B, T, Hk, d = k.shape
-    dev = k.device
-    dt = _dt(k)
-    if v.shape != k.shape or v.dtype != k.dtype:
-        raise ValueError("v must have k's shape and dtype")
-    if k_pages.shape[1] != Hk or k_pages.shape[3] != d:
-        raise ValueError("the cache's heads and channels must be k's")
-    c = _cache(k_pages, v_pages, k_scale, v_scale, page_table, B, dev)
-    kp, kl = _rows(k, "k")
-    vp, vl = _rows(v, "v", dev)
-    _dev_call("muir_kv_append", k, B, T, dt, kp, kl, vp, vl, ctypes.byref(c),
-              _same(start, "start", (B,), torch.int32, dev),
-              _same(count, "count", (B,), torch.int32, dev))
+    (_nat or _native()).kv_append(k, v, k_pages, v_pages, k_scale, v_scale, page_table, start, count)
 
 
 def attn_step(q, k_pages, v_pages, k_scale, v_scale, page_table, lens, scale=None, window=0,
@@ -758,23 +616,8 @@ def attn_step(q, k_pages, v_pages, k_scale, v_scale, page_table, lens, scale=Non
     """One bfloat16 query token ``q [B, Hq, d]`` of every sequence attends over its first
     ``lens[b]`` cached tokens, or the last ``window`` of them (``muir_attn_step``).
     ``scale`` defaults to ``d ** -0.5``.  Returns ``o [B, Hq, d]``."""
-    B, Hq, d = q.shape
-    dev = q.device
-    if k_pages.shape[3] != d:
-        raise ValueError("the cache's channels must be q's")
-    qp = _same(q, "q", (B, Hq, d), torch.bfloat16, dev)
-    if not q.is_cuda:
-        raise ValueError("libmuir takes CUDA tensors only")
-    c = _cache(k_pages, v_pages, k_scale, v_scale, page_table, B, dev)
-    if o is None:
-        o = torch.empty_like(q)
-    op = _same(o, "o", (B, Hq, d), torch.bfloat16, dev)
-    need = (_lib or lib()).muir_attn_step_workspace(B, Hq, ctypes.byref(c))
-    wsb = _workspace(need, dev, ws)
-    _dev_call("muir_attn_step", q, B, Hq, ctypes.byref(c), qp,
-              _same(lens, "lens", (B,), torch.int32, dev), d ** -0.5 if scale is None else scale,
-              window, op, None if wsb is None else wsb.data_ptr(), 0 if wsb is None else wsb.numel())
-    return o
+    return (_nat or _native()).attn_step(q, k_pages, v_pages, k_scale, v_scale, page_table, lens, scale,
+                                         window, o, ws)
 
 
 class MuirChunkFunction(torch.autograd.Function):

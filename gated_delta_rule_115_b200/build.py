@@ -1,4 +1,5 @@
-"""Build libmuir.so in-tree with nvcc for sm_100a.
+"""Build libmuir.so in-tree with nvcc for sm_100a, and the native half of the Python binding
+(``_attn.so``) with g++ against the installed torch.
 
 Usage: ``python -m gated_delta_rule_115_b200.build [--force] [--debug]``.
 The shared library lands next to this file; object files go to ``_build/``.
@@ -38,6 +39,40 @@ def _compile(src: str, obj: str, extra):
     return r.stderr
 
 
+BINDING = os.path.join(HERE, "_attn.so")
+
+
+def build_binding(force: bool = False) -> str:
+    """``csrc/torch_binding.cpp`` -> ``_attn.so``; rebuilt when its sources change or when it
+    was built for another torch."""
+    import sysconfig
+    import torch
+    from torch.utils import cpp_extension
+    src = os.path.join(CSRC, "torch_binding.cpp")
+    stamp = os.path.join(OBJ, "torch_binding.stamp")
+    built_for = f"torch {torch.__version__} python {sysconfig.get_python_version()}"
+    newest = max(os.path.getmtime(p) for p in (src, os.path.join(ROOT, "include", "muir.h")))
+    if (not force and os.path.exists(BINDING) and os.path.getmtime(BINDING) >= newest
+            and os.path.exists(stamp) and open(stamp).read() == built_for):
+        return BINDING
+    os.makedirs(OBJ, exist_ok=True)
+    tmp = BINDING + f".tmp{os.getpid()}"
+    cuda_include = os.path.join(os.path.dirname(os.path.dirname(NVCC)), "include")
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}"]
+    for d in cpp_extension.include_paths() + [cuda_include, sysconfig.get_paths()["include"]]:
+        cmd += ["-isystem", d]
+    cmd += [src, "-o", tmp] + [f"-L{d}" for d in cpp_extension.library_paths()]
+    cmd += ["-lc10", "-lc10_cuda", "-ltorch", "-ltorch_cpu", "-ltorch_cuda", "-ltorch_python"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed for {src}:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, BINDING)
+    with open(stamp, "w") as f:
+        f.write(built_for)
+    return BINDING
+
+
 def build(force: bool = False, debug: bool = False, verbose: bool = False) -> str:
     srcs = sorted(glob.glob(os.path.join(CSRC, "*.cu")))
     os.makedirs(OBJ, exist_ok=True)
@@ -62,6 +97,7 @@ def build(force: bool = False, debug: bool = False, verbose: bool = False) -> st
         if r.returncode != 0:
             raise RuntimeError(f"nvcc link failed:\n{r.stdout}\n{r.stderr}")
         os.replace(tmp, LIB)
+    build_binding(force)
     return LIB
 
 
