@@ -11,10 +11,10 @@ namespace attn {
 constexpr int kTile = 128;    // query or key rows of a product tile
 constexpr int kMaxSeqs = 128; // sequences of one launch (they travel as kernel arguments)
 
-// One sequence: rows [q0, q0 + lq) of the query tensors, [k0, k0 + lk) of the key tensors,
-// and the number of blocks before its own in the launch, for each head.
+// One sequence: rows [q0, q0 + lq) of the query tensors, [k0, k0 + lk) of the key tensors;
+// its blocks for each head, and its entry in the order of the launch's blocks (place_of).
 struct Seq {
-    int q0, lq, k0, lk, block0;
+    int q0, lq, k0, lk, blocks, block0;
 };
 
 // What every kernel needs to know of the call.
@@ -31,14 +31,14 @@ struct Problem {
     int n, Tq, Tk;
     const long long *cu_q, *cu_k;
     Seq seq(int i) const {
-        if (!cu_q) return Seq{i * Tq, Tq, i * Tk, Tk, 0};
-        return Seq{(int)cu_q[i], (int)(cu_q[i + 1] - cu_q[i]), (int)cu_k[i], (int)(cu_k[i + 1] - cu_k[i]), 0};
+        if (!cu_q) return Seq{i * Tq, Tq, i * Tk, Tk, 0, 0};
+        return Seq{(int)cu_q[i], (int)(cu_q[i + 1] - cu_q[i]), (int)cu_k[i], (int)(cu_k[i + 1] - cu_k[i]), 0, 0};
     }
 };
 
 // Sequences [first, last) of the call (at most kMaxSeqs) whose `rows` (queries, or keys with
 // by_keys) number at least one, the longest first, with their blocks of rows_per_block rows
-// counted into block0.  Returns how many; `blocks`: the total.
+// and the order of these.  Returns how many; `blocks`: the total.
 int gather_seqs(const Problem& p, int first, int last, bool by_keys, int rows_per_block, Seq* out,
                 long long* blocks);
 

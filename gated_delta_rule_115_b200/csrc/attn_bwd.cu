@@ -98,7 +98,7 @@ struct DkvSmem {
     static constexpr int kRing = 2 * kTileBytes;                       // after the two resident tiles
     static constexpr int kVec = kRing + kStages * 2 * kTileBytes;      // -lse log2 e and D of a stage's rows
     static constexpr int kBars = kVec + kStages * 2 * kTile * 4;
-    static constexpr int kBytes = kBars + 256;
+    static constexpr int kBytes = kBars + 512;
 };
 
 // Whole-warp bounded wait.
@@ -139,7 +139,10 @@ struct DkvBars {
     uint64_t full[NS], empty[NS], tail;
     // of each half of the columns:
     uint64_t s_full[2], dp_full[2];             // its products of a step in tensor memory
-    uint64_t p_full[2], dp_read[2], ds_full[2]; // four warps: p written, P read, ds written
+    // Four warps: p written (of even, of odd steps: a half may write its next p before the
+    // other lets the sums' warp come to this one, and a barrier two phases on looks as if it
+    // had not moved), P read, ds written.
+    uint64_t p_full[4], dp_read[2], ds_full[2];
     uint64_t acc_done[2];                       // its last product of a step
     uint64_t final_done;
     uint32_t tmem_slot;
@@ -161,8 +164,9 @@ __device__ __forceinline__ void dkv_block(const BwdParams& p, unsigned char* sm,
     static_assert(sizeof(DkvBars<NS>) <= SM::kBytes - SM::kBars, "barriers");
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const Seq sq = p.kv[find_seq(p.kv, p.n_kv, blk)];
-    const int kb = blk - sq.block0;  // with a causal mask the first keys are seen most
+    const Place place = place_of(p.kv, p.n_kv, blk);
+    const Seq sq = place.sq;
+    const int kb = sq.blocks - 1 - place.rank;  // with a causal mask the first keys are seen most
     const int G = p.group;
     const int off = sq.lk - sq.lq;
     const int k0 = kb * kTile;
@@ -189,6 +193,7 @@ __device__ __forceinline__ void dkv_block(const BwdParams& p, unsigned char* sm,
             mbar_init(bar->s_full + i, 1);
             mbar_init(bar->dp_full + i, 1);
             mbar_init(bar->p_full + i, 4);
+            mbar_init(bar->p_full + 2 + i, 4);
             mbar_init(bar->dp_read + i, 4);
             mbar_init(bar->ds_full + i, 4);
             mbar_init(bar->acc_done + i, 1);
@@ -292,7 +297,7 @@ __device__ __forceinline__ void dkv_block(const BwdParams& p, unsigned char* sm,
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
                     const uint32_t x = tmem + 128u * u + (uint32_t)(j & 1) * 64u;
-                    ok = ok && mbar_wait(bar->p_full + u, j & 1);
+                    ok = ok && mbar_wait(bar->p_full + 2 * u + (j & 1), (j >> 1) & 1);
                     if (!ok) break;
                     tc_fence_after();
 #pragma unroll
@@ -363,7 +368,7 @@ __device__ __forceinline__ void dkv_block(const BwdParams& p, unsigned char* sm,
             tmem_wait_st();
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(bar->p_full + wg);
+            if (lane == 0) mbar_arrive(bar->p_full + 2 * wg + (j & 1));
 
             ok = warp_wait(bar->dp_full + wg, j & 1);
             if (!ok) break;
@@ -453,9 +458,9 @@ __device__ __forceinline__ void dq_block(const BwdParams& p, unsigned char* sm, 
     static_assert(sizeof(DqBars<NK, NV>) <= SM::kBytes - SM::kBars, "barriers");
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const Seq sq = p.q[find_seq(p.q, p.n_q, blk)];
-    const int nblk = (sq.lq + kTile - 1) / kTile;
-    const int qb = nblk - 1 - (blk - sq.block0);
+    const Place place = place_of(p.q, p.n_q, blk);
+    const Seq sq = place.sq;
+    const int qb = place.rank;
     const int off = sq.lk - sq.lq;
     const int r0 = qb * kTile, r1 = min(r0 + kTile, sq.lq) - 1;
 

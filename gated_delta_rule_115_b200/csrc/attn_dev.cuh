@@ -173,6 +173,7 @@ __device__ __forceinline__ void store_rows(uint32_t tsrc, float f, bool any, uns
         for (int k = 0; k < U; ++k)
             if (rr0 + (i + k) * RPI < rows) *reinterpret_cast<uint4*>(out + (long long)(i + k) * RPI * ld) = v[k];
     }
+    __syncwarp();  // the warp's rows of the tile may be written again
 }
 
 // Blocks of a launch lie on the grid as (head, block % 65535, block / 65535): no division
@@ -188,15 +189,24 @@ __device__ __forceinline__ int block_index() { return (int)(blockIdx.y + kGridY 
 // where half a head's distance to the next integer is 1 / (2 group)).
 __device__ __forceinline__ int key_head(int h, float inv_group) { return (int)(((float)h + 0.5f) * inv_group); }
 
-// The sequence that block `i` belongs to (block0 ascending, the first 0).
-__device__ __forceinline__ int find_seq(const Seq* s, int n, int i) {
+// Block `blk` of a launch: its sequence, and its place in it counted so that a larger `rank`
+// has more work under a causal mask.  Blocks come by rank, the largest first, and at one rank
+// by sequence (the longest first): whichever order they end in, the last ones are short.  With
+// sequence k the k-th longest, ranks from its number of blocks up to the one before's hold k
+// blocks each, and the first of them is block seqs[k - 1].block0.
+struct Place {
+    Seq sq;
+    int rank;
+};
+__device__ __forceinline__ Place place_of(const Seq* seqs, int n, int blk) {
     int lo = 0, hi = n - 1;
     while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
-        if (s[mid].block0 <= i) lo = mid;
+        if (seqs[mid].block0 <= blk) lo = mid;
         else hi = mid - 1;
     }
-    return lo;
+    const unsigned i = (unsigned)(blk - seqs[lo].block0), level = i / (unsigned)(lo + 1);
+    return {seqs[i - level * (lo + 1)], seqs[lo].blocks - 1 - (int)level};
 }
 
 }  // namespace attn

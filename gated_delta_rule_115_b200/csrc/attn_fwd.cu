@@ -83,12 +83,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fwd(const __grid_constant_
     const int blk = block_index(), h = p.by_heads ? 2 * blockIdx.x : blockIdx.x;
     const int dh = p.by_heads ? 1 : 0, dt = 1 - dh;  // from one of the block's tiles to the next
     if (blk >= p.blocks) return;
-    const Seq sq = p.seq[find_seq(p.seq, p.n, blk)];
-    // the longest rows of a causal sequence first
-    const int wide = p.tiles == 2 && !p.by_heads ? 1 : 0;
-    const int nblk = (sq.lq + (kTile << wide) - 1) >> (7 + wide);
-    static_assert(kTile == 128, "shift");
-    const int qt = (nblk - 1 - (blk - sq.block0)) << wide;  // its first query tile
+    const Place place = place_of(p.seq, p.n, blk);
+    const Seq sq = place.sq;
+    const int qt = place.rank << (p.tiles == 2 && !p.by_heads ? 1 : 0);  // its first query tile
     const int hk = key_head(h, p.inv_group);
     const int off = sq.lk - sq.lq;
 
@@ -393,10 +390,12 @@ int gather_seqs(const Problem& p, int first, int last, bool by_keys, int rows_pe
         const int lx = by_keys ? x.lk : x.lq, ly = by_keys ? y.lk : y.lq;
         return lx != ly ? lx > ly : x.q0 < y.q0;
     });
+    for (int k = 0; k < n; ++k)
+        out[k].blocks = ((by_keys ? out[k].lk : out[k].lq) + rows_per_block - 1) / rows_per_block;
     long long total = 0;
     for (int k = 0; k < n; ++k) {
         out[k].block0 = (int)total;
-        total += ((by_keys ? out[k].lk : out[k].lq) + rows_per_block - 1) / rows_per_block;
+        total += (long long)(k + 1) * (out[k].blocks - (k + 1 < n ? out[k + 1].blocks : 0));
     }
     *blocks = total;
     return n;

@@ -261,3 +261,18 @@ def test_gradients_by_differences(m):
     assert abs(float(f[0] - f[1]) - slope) <= tol
     # and the bound means something: the slope itself is several times larger
     assert abs(slope) > 2 * tol
+
+
+@pytest.mark.parametrize("d,Hq,Hk", [(64, 16, 4), (128, 8, 8)])
+def test_many_launches(m, d, Hq, Hk):
+    """Hundreds of launches in a row give one result, and no wait inside them runs out: the
+    two halves of a block's columns may drift apart by more than a step."""
+    q, do = (rnd(4, 640, Hq, d, seed=s).cuda() for s in (1, 4))
+    k, v = (rnd(4, 640, Hk, d, seed=s).cuda() for s in (2, 3))
+    o, lse = m.attn_fwd(q, k, v)
+    g = m.attn_bwd(q, k, v, o, lse, do)
+    for _ in range(600):
+        o2, lse2 = m.attn_fwd(q, k, v)
+        g2 = m.attn_bwd(q, k, v, o, lse, do)
+    m.device_wait_status()
+    assert torch.equal(o, o2) and torch.equal(lse, lse2) and all(torch.equal(g[n], g2[n]) for n in g)
