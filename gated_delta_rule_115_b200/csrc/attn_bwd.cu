@@ -101,6 +101,12 @@ struct DkvSmem {
     static constexpr int kBytes = kBars + 512;
 };
 
+// How many of a sequence's lk keys the query at key position `at` sees.
+__device__ __forceinline__ int keys_seen(int causal, int window, int lk, int at) {
+    const int last = causal ? min(lk - 1, at) : lk - 1, first = window ? max(0, at - window + 1) : 0;
+    return max(0, last - first + 1);
+}
+
 // Whole-warp bounded wait.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity) {
     return __all_sync(0xffffffffu, mbar_wait(bar, parity)) != 0;
@@ -322,6 +328,7 @@ __device__ __forceinline__ void dkv_block(const BwdParams& p, unsigned char* sm,
         const int wg = warp >> 2;
         const uint32_t lane0 = (uint32_t)(warp & 3) << 21;
         const int key = k0 + (threadIdx.x & 127);  // the thread's row
+        const bool all_single = p.window == 1 || sq.lk == 1;  // no query sees two keys
         const float c = p.scale_log2;
         bool ok = true;
         int tile = 0;  // of step j
@@ -337,6 +344,8 @@ __device__ __forceinline__ void dkv_block(const BwdParams& p, unsigned char* sm,
             const int sees = key - off - i0 - 64 * wg;
             const bool before = p.causal && i0 + off < k0 + kTile - 1;
             const bool behind = p.window && i0 + kTile - 1 + off - p.window >= k0;
+            // the column of a causal sequence's first position, whose query sees one key only
+            const int single = p.causal ? -off - i0 - 64 * wg : -1;
             ok = warp_wait(bar->s_full + wg, j & 1) && warp_wait(bar->full + j % NS, (j / NS) & 1);
             if (!ok) break;
             tc_fence_after();
@@ -370,6 +379,12 @@ __device__ __forceinline__ void dkv_block(const BwdParams& p, unsigned char* sm,
             __syncwarp();
             if (lane == 0) mbar_arrive(bar->p_full + 2 * wg + (j & 1));
 
+            // A query that sees one key gives it weight 1 whatever their score: ds is zero, where
+            // dO . v and D, which are then the same, differ by their roundings.
+            if (all_single || (single >= 0 && single < 64)) {
+#pragma unroll
+                for (int i = 0; i < 64; ++i) s[i >> 5][i & 31] = all_single || i == single ? 0.f : s[i >> 5][i & 31];
+            }
             ok = warp_wait(bar->dp_full + wg, j & 1);
             if (!ok) break;
             tc_fence_after();
@@ -620,11 +635,13 @@ __device__ __forceinline__ void dq_block(const BwdParams& p, unsigned char* sm, 
         const int kmin = p.window ? at - p.window + 1 : 0;
         const int all_max = p.causal ? min(sq.lk - 1, r0 + off) : sq.lk - 1;
         const int all_min = p.window ? r0 + kTile - 1 + off - p.window + 1 : 0;
-        // rows that do not exist and queries that see no key: no weight
+        // Rows that do not exist and queries that see no key: no weight.  Nor for queries that
+        // see one: their ds is zero.
+        const bool some = row < sq.lq && keys_seen(p.causal, p.window, sq.lk, at) > 1;
         float nls[2] = {-INFINITY, -INFINITY}, dls[2] = {0.f, 0.f};
 #pragma unroll
         for (int n = 0; n < SM::kHeads; ++n)
-            if (row < sq.lq && n <= sh) {
+            if (some && n <= sh) {
                 const long long v = sq.q0 * p.lse_seq + (h + n) * p.lse_head + row;
                 const float e = p.lse[v];
                 if (e != -INFINITY) nls[n] = -e * kLog2e;

@@ -276,3 +276,27 @@ def test_many_launches(m, d, Hq, Hk):
         g2 = m.attn_bwd(q, k, v, o, lse, do)
     m.device_wait_status()
     assert torch.equal(o, o2) and torch.equal(lse, lse2) and all(torch.equal(g[n], g2[n]) for n in g)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_one_visible_key_has_no_score_gradient(m, d):
+    """A weight of 1 does not depend on its score: dq and what it adds to dk are exactly
+    zero, and dv is dO's (rounded) sum."""
+    for lens, causal, window in (([1, 1, 1], True, 0), ([1, 300, 1], True, 0), ([200, 130], True, 1), ([1], False, 0)):
+        cu, _ = spans(lens)
+        q, k, v, do = (rnd(1, cu[-1], H, d, seed=s).cuda() for s, H in ((1, 4), (2, 2), (3, 2), (4, 4)))
+        o, lse = m.attn_fwd_varlen(q, k, v, cu, causal=causal, window=window)
+        g = m.attn_bwd_varlen(q, k, v, o, lse, do, cu, causal=causal, window=window)
+        for a, b in zip(cu, cu[1:]):
+            rows = slice(a, b) if window == 1 or b - a == 1 else slice(a, a + 1)
+            assert not g["dq"][0, rows].any() and torch.equal(o[0, rows], v[0, rows].repeat_interleave(2, 1))
+            if window == 1 or b - a == 1:
+                assert not g["dk"][0, rows].any()
+                want = do[0, rows].double().unflatten(1, (2, 2)).sum(2)
+                assert ((g["dv"][0, rows].double() - want).abs() <= U * want.abs() + 1e-6).all()
+    # one key, many queries
+    q, k, v, do = (rnd(1, T, H, d, seed=s).cuda() for s, T, H in ((1, 50, 4), (2, 1, 2), (3, 1, 2), (4, 50, 4)))
+    o, lse = m.attn_fwd(q, k, v, causal=False)
+    g = m.attn_bwd(q, k, v, o, lse, do, causal=False)
+    assert not g["dq"].any() and not g["dk"].any()
+    m.device_wait_status()
