@@ -44,7 +44,7 @@ constexpr float kLog2e = 1.4426950408889634f;
 
 struct BwdParams {
     CUtensorMap tq, tk, tv, tdo;
-    const float *lse, *delta;
+    const float *lse, *delta, *few;
     __nv_bfloat16 *dq, *dk, *dv;
     long long lse_seq, lse_head;
     float scale, scale_log2;
@@ -56,36 +56,112 @@ struct BwdParams {
 
 // ------------------------------------------------------------------ D = dO . o
 
-// A row of D channels is D / 8 lanes; one float32 a (token, head).
+// D enters every ds of its row, so an error of it does not average out over the keys as the
+// roundings of p do.  From the o that the forward pass rounded to bf16 it is off by up to
+// 2^-8 sum |dO||o|, which matters where few keys share a row's weight (|o| is then as large
+// as |v|): two visible keys leave 0.0038 in dq where everything else leaves 0.0023, sixteen
+// 0.0029.  Rows of up to kFewKeys keys take D = sum_j p_j dO . v_j instead, in float32.
+constexpr int kFewKeys = 8;
+
+struct DeltaParams {
+    const __nv_bfloat16 *o, *dO, *q, *k, *v;
+    long long q_ld, k_ld, v_ld;
+    const float* lse;
+    float *delta, *few;  // D = dO . o of every row; D of the rows of few keys, at the same places
+    long long lse_seq, lse_head;
+    float scale_log2, inv_group;
+    int Hq, T, causal, window;
+    long long rows;      // (token, head) pairs
+    int few_blocks, few_rows;
+    int n;               // sequences with rows of few keys
+    struct {
+        int q0, lq, k0, lk, first, row0;  // their first such row, and how many come before it
+    } seq[kMaxSeqs];
+};
+
+// How many of a sequence's lk keys the query at key position `at` sees.
+__device__ __forceinline__ int keys_seen(int causal, int window, int lk, int at) {
+    const int last = causal ? min(lk - 1, at) : lk - 1, first = window ? max(0, at - window + 1) : 0;
+    return max(0, last - first + 1);
+}
+
+__device__ __forceinline__ void unpack8(const __nv_bfloat16* p, float (&v)[8]) {
+    const uint4 u = *reinterpret_cast<const uint4*>(p);
+    unpack16<true>(u.x, v[0], v[1]);
+    unpack16<true>(u.y, v[2], v[3]);
+    unpack16<true>(u.z, v[4], v[5]);
+    unpack16<true>(u.w, v[6], v[7]);
+}
+
+// A row (token, head) of D channels is D / 8 lanes.  The first blocks take the rows of few
+// keys, beside the others, which read o and dO once and are bound by HBM.
 template <int D>
-__global__ void __launch_bounds__(256) k_attn_delta(const __nv_bfloat16* __restrict__ o,
-                                                    const __nv_bfloat16* __restrict__ dO, float* __restrict__ delta,
-                                                    long long rows, int Hq, int T, long long lse_seq,
-                                                    long long lse_head) {
-    constexpr int G = D / 8;
-    const int lane = threadIdx.x & 31, sub = lane / G;
-    const long long r = ((long long)blockIdx.x * 8 + (threadIdx.x >> 5)) * (32 / G) + sub;
-    float s = 0.f;
-    if (r < rows) {
-        const uint4 a = *reinterpret_cast<const uint4*>(o + r * D + (lane % G) * 8);
-        const uint4 b = *reinterpret_cast<const uint4*>(dO + r * D + (lane % G) * 8);
-        const uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w};
+__global__ void __launch_bounds__(256, 6) k_attn_delta(const __grid_constant__ DeltaParams p) {
+    constexpr int G = D / 8, RPW = 32 / G;
+    const int lane = threadIdx.x & 31, sub = (threadIdx.x >> 5) * RPW + lane / G, ch = (lane % G) * 8;
+    auto row_sum = [](float s) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            float x0, x1, y0, y1;
-            unpack16<true>(x[i], x0, x1);
-            unpack16<true>(y[i], y0, y1);
-            s += x0 * y0 + x1 * y1;
+        for (int off = G / 2; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
+        return s;
+    };
+    if ((int)blockIdx.x < p.few_blocks) {
+        const long long r = (long long)blockIdx.x * (8 * RPW) + sub, x = r / p.Hq;
+        const bool on = x < p.few_rows;
+        const int h = (int)(r - x * p.Hq), hk = key_head(h, p.inv_group);
+        int lo = 0, hi = p.n - 1;
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (p.seq[mid].row0 <= (int)x) lo = mid;
+            else hi = mid - 1;
         }
-    }
+        const int pos = on ? p.seq[lo].first + (int)x - p.seq[lo].row0 : 0;
+        const int at = pos + p.seq[lo].lk - p.seq[lo].lq;
+        const int seen = on ? keys_seen(p.causal, p.window, p.seq[lo].lk, at) : 0;
+        const bool few = seen > 1 && seen <= kFewKeys;
+        const long long tok = p.seq[lo].q0 + pos, out = p.seq[lo].q0 * p.lse_seq + h * p.lse_head + pos;
+        const long long key = p.seq[lo].k0 + (p.window ? max(0, at - p.window + 1) : 0);
+        float q[8] = {}, g[8] = {}, e = 0.f, sum = 0.f;
+        if (few) {
+            unpack8(p.q + tok * p.q_ld + h * D + ch, q);
+            unpack8(p.dO + (tok * p.Hq + h) * D + ch, g);
+            e = p.lse[out] * kLog2e;
+        }
+#pragma unroll 4
+        for (int j = 0; j < kFewKeys; ++j) {
+            float sc = 0.f, dp = 0.f;
+            if (few && j < seen) {
+                float k[8], v[8];
+                unpack8(p.k + (key + j) * p.k_ld + hk * D + ch, k);
+                unpack8(p.v + (key + j) * p.v_ld + hk * D + ch, v);
 #pragma unroll
-    for (int off = G / 2; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
-    if (r < rows && lane % G == 0) {
+                for (int c = 0; c < 8; ++c) {
+                    sc += q[c] * k[c];
+                    dp += g[c] * v[c];
+                }
+            }
+            sc = row_sum(sc);
+            dp = row_sum(dp);
+            if (few && j < seen) sum += ex2(sc * p.scale_log2 - e) * dp;
+        }
+        if (few && lane % G == 0) p.few[out] = sum;
+        return;
+    }
+    const long long r = (long long)(blockIdx.x - p.few_blocks) * (8 * RPW) + sub;
+    float s = 0.f;
+    if (r < p.rows) {
+        float x[8], y[8];
+        unpack8(p.o + r * D + ch, x);
+        unpack8(p.dO + r * D + ch, y);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) s += x[i] * y[i];
+    }
+    s = row_sum(s);
+    if (r < p.rows && lane % G == 0) {
         // token-major rows -> the layout of lse
-        const long long tok = r / Hq;
-        const int h = (int)(r - tok * Hq);
-        const long long b = lse_seq == 1 ? 0 : tok / T;
-        delta[b * T * lse_seq + h * lse_head + (tok - b * T)] = s;
+        const long long tok = r / p.Hq;
+        const int h = (int)(r - tok * p.Hq);
+        const long long b = p.lse_seq == 1 ? 0 : tok / p.T;
+        p.delta[b * p.T * p.lse_seq + h * p.lse_head + (tok - b * p.T)] = s;
     }
 }
 
@@ -100,12 +176,6 @@ struct DkvSmem {
     static constexpr int kBars = kVec + kStages * 2 * kTile * 4;
     static constexpr int kBytes = kBars + 512;
 };
-
-// How many of a sequence's lk keys the query at key position `at` sees.
-__device__ __forceinline__ int keys_seen(int causal, int window, int lk, int at) {
-    const int last = causal ? min(lk - 1, at) : lk - 1, first = window ? max(0, at - window + 1) : 0;
-    return max(0, last - first + 1);
-}
 
 // Whole-warp bounded wait.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity) {
@@ -232,24 +302,33 @@ __device__ __forceinline__ void dkv_block(const BwdParams& p, unsigned char* sm,
                 tile = 0;
                 ++head;
             }
+            // -lse log2 e and D of the tile's queries; -infinity (no weight at all) for rows
+            // that do not exist and for queries that see no key; asked for before the stage is free
+            const long long at = sq.q0 * p.lse_seq + h * p.lse_head + i0;
+            const bool any_few = (p.window && p.window <= kFewKeys) || sq.lk <= kFewKeys ||
+                                 (p.causal && i0 + off < kFewKeys);
+            float e[kTile / 32], dd[kTile / 32];
+#pragma unroll
+            for (int n = 0; n < kTile / 32; ++n) {
+                const int x = lane + 32 * n;
+                const bool on = i0 + x < sq.lq;
+                const float* from = p.delta;
+                if (any_few && keys_seen(p.causal, p.window, sq.lk, i0 + x + off) <= kFewKeys) from = p.few;
+                e[n] = on ? p.lse[at + x] : -INFINITY;
+                dd[n] = on ? from[at + x] : 0.f;
+            }
             if (i >= NS) ok = warp_wait(bar->empty + st, (i / NS - 1) & 1);
             if (!ok) break;
             ok = load_pair<D>(sm + SM::kRing + st * 2 * SM::kTileBytes, &p.tq, &p.tdo, h, sq.q0 + i0, sq.lq - i0,
                               bar->full + st, &bar->tail, tails);
-            // -lse log2 e and D of the tile's queries; -infinity (no weight at all) for rows
-            // that do not exist and for queries that see no key
             float* v = vec + st * 2 * kTile;
-            const long long at = sq.q0 * p.lse_seq + h * p.lse_head + i0;
 #pragma unroll
-            for (int x = lane; x < kTile; x += 32) {
-                float a = -INFINITY, b = 0.f;
-                if (i0 + x < sq.lq) {
-                    const float e = p.lse[at + x];
-                    a = e == -INFINITY ? -INFINITY : -e * kLog2e;
-                    b = p.delta[at + x];
-                }
-                v[x] = a;
-                v[kTile + x] = b;
+            for (int n = 0; n < kTile / 32; ++n) {
+                const int x = lane + 32 * n;
+                // of one key or none: ds is zero, and D has not been formed
+                if (any_few && keys_seen(p.causal, p.window, sq.lk, i0 + x + off) <= 1) dd[n] = 0.f;
+                v[x] = e[n] == -INFINITY ? -INFINITY : -e[n] * kLog2e;
+                v[kTile + x] = dd[n];
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(bar->full + st);
@@ -637,7 +716,8 @@ __device__ __forceinline__ void dq_block(const BwdParams& p, unsigned char* sm, 
         const int all_min = p.window ? r0 + kTile - 1 + off - p.window + 1 : 0;
         // Rows that do not exist and queries that see no key: no weight.  Nor for queries that
         // see one: their ds is zero.
-        const bool some = row < sq.lq && keys_seen(p.causal, p.window, sq.lk, at) > 1;
+        const int seen = keys_seen(p.causal, p.window, sq.lk, at);
+        const bool some = row < sq.lq && seen > 1;
         float nls[2] = {-INFINITY, -INFINITY}, dls[2] = {0.f, 0.f};
 #pragma unroll
         for (int n = 0; n < SM::kHeads; ++n)
@@ -645,7 +725,7 @@ __device__ __forceinline__ void dq_block(const BwdParams& p, unsigned char* sm, 
                 const long long v = sq.q0 * p.lse_seq + (h + n) * p.lse_head + row;
                 const float e = p.lse[v];
                 if (e != -INFINITY) nls[n] = -e * kLog2e;
-                dls[n] = p.delta[v];
+                dls[n] = (seen <= kFewKeys ? p.few : p.delta)[v];
             }
         const float c = p.scale_log2;
         bool ok = true;
@@ -740,13 +820,45 @@ cudaError_t run(const Problem& p, BwdParams& a, const void* o, const void* dO, f
     static std::atomic<uint64_t> done{0};
     cudaError_t err = allow_smem(k_attn_bwd<D>, kSmem, done);
     if (err != cudaSuccess) return err;
-    if (p.q_rows > 0) {
-        const long long rows = p.q_rows * p.Hq;
-        constexpr int kRowsPerBlock = 8 * (32 / (D / 8));
-        MUIR_TIMED("k_attn_delta", st,
-                   k_attn_delta<D><<<(unsigned)((rows + kRowsPerBlock - 1) / kRowsPerBlock), 256, 0, st>>>(
-                       static_cast<const __nv_bfloat16*>(o), static_cast<const __nv_bfloat16*>(dO), delta, rows,
-                       p.Hq, p.Tq, p.lse_seq, p.lse_head));
+    DeltaParams d;
+    d.o = static_cast<const __nv_bfloat16*>(o);
+    d.dO = static_cast<const __nv_bfloat16*>(dO);
+    d.q = static_cast<const __nv_bfloat16*>(p.q);
+    d.k = static_cast<const __nv_bfloat16*>(p.k);
+    d.v = static_cast<const __nv_bfloat16*>(p.v);
+    d.q_ld = p.q_ld; d.k_ld = p.k_ld; d.v_ld = p.v_ld;
+    d.lse = a.lse;
+    d.delta = delta;
+    d.few = delta + p.q_rows * p.Hq;
+    d.lse_seq = p.lse_seq; d.lse_head = p.lse_head;
+    d.scale_log2 = a.scale_log2;
+    d.inv_group = (float)p.Hk / (float)p.Hq;
+    d.Hq = p.Hq; d.T = p.Tq; d.causal = p.causal; d.window = p.window;
+    constexpr int kRowsPerBlock = 8 * (32 / (D / 8));
+    for (int i = 0; i < p.n && p.q_rows > 0; i += kMaxSeqs) {
+        // every row with the first launch, and each launch's sequences' rows of few keys
+        d.rows = i == 0 ? p.q_rows * p.Hq : 0;
+        d.n = 0;
+        long long few_rows = 0;
+        for (int x = i; x < std::min(i + kMaxSeqs, p.n); ++x) {
+            const Seq s = p.seq(x);
+            const int off = s.lk - s.lq;
+            int first = 0, end = 0;
+            if ((p.window && p.window <= kFewKeys) || s.lk <= kFewKeys) {
+                end = s.lq;
+            } else if (p.causal) {  // positions 1 .. kFewKeys - 1
+                first = std::max(0, 1 - off);
+                end = std::min(s.lq, kFewKeys - off);
+            }
+            if (end <= first || s.lk < 2) continue;
+            d.seq[d.n++] = {s.q0, s.lq, s.k0, s.lk, first, (int)few_rows};
+            few_rows += end - first;
+        }
+        d.few_rows = (int)few_rows;
+        d.few_blocks = (int)((few_rows * p.Hq + kRowsPerBlock - 1) / kRowsPerBlock);
+        const unsigned blocks = (unsigned)(d.few_blocks + (d.rows + kRowsPerBlock - 1) / kRowsPerBlock);
+        if (blocks == 0) continue;
+        MUIR_TIMED("k_attn_delta", st, k_attn_delta<D><<<blocks, 256, 0, st>>>(d));
         if ((err = cudaGetLastError()) != cudaSuccess) return err;
     }
     for (int i = 0; i < p.n; i += kMaxSeqs) {
@@ -770,7 +882,7 @@ cudaError_t run(const Problem& p, BwdParams& a, const void* o, const void* dO, f
 
 }  // namespace
 
-size_t bwd_ws_bytes(const Problem& p) { return (size_t)p.q_rows * p.Hq * 4; }
+size_t bwd_ws_bytes(const Problem& p) { return (size_t)p.q_rows * p.Hq * 8; }
 
 cudaError_t run_bwd(const Problem& p, const void* o, const float* lse, const void* dO, void* dq, void* dk,
                     void* dv, void* ws, cudaStream_t st) {
@@ -788,6 +900,7 @@ cudaError_t run_bwd(const Problem& p, const void* o, const float* lse, const voi
     if (err != cudaSuccess) return err;
     a.lse = lse;
     a.delta = static_cast<float*>(ws);
+    a.few = a.delta + p.q_rows * p.Hq;
     a.dq = static_cast<__nv_bfloat16*>(dq);
     a.dk = static_cast<__nv_bfloat16*>(dk);
     a.dv = static_cast<__nv_bfloat16*>(dv);

@@ -422,7 +422,7 @@ muir_status muir_rotary(int B, int T, int Hq, int Hk, int d, int rot, muir_dtype
  * tensor cores: 4 d flops a visible pair forward, 10 d backward.
  *
  * muir_attn_bwd: gradients of sum(o * dO).  o and lse are the forward's; the
- * probabilities are recomputed from lse.  Workspace: one float32 a query and head.
+ * probabilities are recomputed from lse.  Workspace: two float32 a query and head.
  *
  * The varlen forms take num_seqs sequences packed in one buffer, as muir_chunk_fwd_varlen
  * does: B = 1, Tq and Tk total tokens, cu_q and cu_k HOST arrays of num_seqs + 1 offsets

@@ -7,7 +7,8 @@ Tolerances per element, from the arithmetic.  u = 2^-8 is half a bfloat16 step.
   lse : 64 2^-21 = 3e-5
   dv  : the same with dO for v;  lse adds 3e-5 to a weight
   dq, dk : u |dq|; u sum |ds||k| for ds rounded as an operand, 2e-4 of it for p; D = dO.o
-        from a bfloat16 o: u sum p (sum |dO||o|) scale |k|, with a kernel's own o another
+        from a bfloat16 o (rows of more than 8 keys; fewer take it in float32, which is
+        smaller): u sum p (sum |dO||o|) scale |k|, with a kernel's own o another
         u sum p (sum |dO| sum p |v|) scale |k|; dO.v and D as float32 sums of 128 products:
         2^-17 of sum p (sum |dO||v|) scale |k|"""
 import numpy as np
@@ -299,4 +300,22 @@ def test_one_visible_key_has_no_score_gradient(m, d):
     o, lse = m.attn_fwd(q, k, v, causal=False)
     g = m.attn_bwd(q, k, v, o, lse, do, causal=False)
     assert not g["dq"].any() and not g["dk"].any()
+    m.device_wait_status()
+
+
+@pytest.mark.parametrize("T,window,Hq,Hk,d", [(2, 0, 4, 2, 64), (5, 0, 2, 2, 128), (8, 0, 6, 2, 64), (300, 2, 2, 1, 128),
+                                              (300, 8, 3, 3, 64)])
+def test_rows_of_few_keys(m, T, window, Hq, Hk, d):
+    """Up to eight visible keys: D comes from the keys themselves, and a rounded o adds
+    nothing to the gradients."""
+    q, k, v, do = (rnd(3, T, H, d, seed=s) for s, H in ((1, Hq), (2, Hk), (3, Hk), (4, Hq)))
+    dev = [t.cuda() for t in (q, k, v, do)]
+    o, lse = m.attn_fwd(*dev[:3], window=window)
+    g = m.attn_bwd(*dev[:3], o, lse, dev[3], window=window)
+    wrong = m.attn_bwd(*dev[:3], torch.zeros_like(o), lse, dev[3], window=window)
+    assert all(torch.equal(g[n], wrong[n]) for n in g)  # o is not read for these rows' D
+    for b, r in enumerate(oracle(q, k, v, do, [(b, b) for b in range(3)], window=window)):
+        for n in ("dq", "dk"):
+            tol = U * np.abs(r[n]) + (U + 2e-4) * r[n + "_abs"] + 2.0 ** -17 * r[n + "_dp"]
+            within(g[n][b], r[n], tol, n)
     m.device_wait_status()

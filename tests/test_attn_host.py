@@ -176,7 +176,7 @@ def test_attention_refusals(m, over, code):
 
 @pytest.mark.parametrize("over,code", [
     (dict(dO=None), INVALID), (dict(dq=FAKE + 4), INVALID), (dict(dk=None), INVALID), (dict(dv=None), INVALID),
-    (dict(ws=None), WORKSPACE), (dict(ws_bytes=8 * 4 * 4 - 1), WORKSPACE)])
+    (dict(ws=None), WORKSPACE), (dict(ws_bytes=8 * 4 * 8 - 1), WORKSPACE)])
 def test_attention_backward_refusals(m, over, code):
     assert attn(m, True, **over) == code
 
@@ -198,6 +198,6 @@ def test_attention_varlen_refusals(m, cu, ck, over, code):
 
 def test_attention_workspace(m):
     s = m.MuirAttnShape(2, 100, 50, 4, 2, 64, 1, 0, 0.125, 0, 0, 0)
-    assert m.lib().muir_attn_bwd_workspace(ctypes.byref(s)) == 2 * 100 * 4 * 4
+    assert m.lib().muir_attn_bwd_workspace(ctypes.byref(s)) == 2 * 100 * 4 * 8
     s.d = 32
     assert m.lib().muir_attn_bwd_workspace(ctypes.byref(s)) == 0
