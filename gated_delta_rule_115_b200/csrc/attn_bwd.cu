@@ -98,6 +98,7 @@ __device__ __forceinline__ void unpack8(const __nv_bfloat16* p, float (&v)[8]) {
 template <int D>
 __global__ void __launch_bounds__(256, 6) k_attn_delta(const __grid_constant__ DeltaParams p) {
     constexpr int G = D / 8, RPW = 32 / G;
+    grid_release();  // the next kernel's blocks set themselves up meanwhile
     const int lane = threadIdx.x & 31, sub = (threadIdx.x >> 5) * RPW + lane / G, ch = (lane % G) * 8;
     auto row_sum = [](float s) {
 #pragma unroll
@@ -295,6 +296,7 @@ __device__ __forceinline__ void dkv_block(const BwdParams& p, unsigned char* sm,
         bool ok = true;
         uint32_t tails = 0;
         int tile = 0, head = 0;  // of step i
+        grid_wait();             // for D
         for (int i = 0; i < steps && ok; ++i) {
             const int st = i % NS, i0 = (lo + tile) * kTile;
             const int h = hk * G + head;
@@ -716,6 +718,7 @@ __device__ __forceinline__ void dq_block(const BwdParams& p, unsigned char* sm, 
         const int all_min = p.window ? r0 + kTile - 1 + off - p.window + 1 : 0;
         // Rows that do not exist and queries that see no key: no weight.  Nor for queries that
         // see one: their ds is zero.
+        grid_wait();  // for D
         const int seen = keys_seen(p.causal, p.window, sq.lk, at);
         const bool some = row < sq.lq && seen > 1;
         float nls[2] = {-INFINITY, -INFINITY}, dls[2] = {0.f, 0.f};
@@ -874,8 +877,9 @@ cudaError_t run(const Problem& p, BwdParams& a, const void* o, const void* dO, f
         a.dq_heads = DqSmem<D>::kHeads == 2 && a.group % 2 == 0 && q_blocks * (p.Hq / 2) >= 2 * kSMs ? 2 : 1;
         const long long blocks = kv_blocks + q_blocks * (a.group / a.dq_heads);
         if (blocks == 0) continue;
-        MUIR_TIMED("k_attn_bwd", st, k_attn_bwd<D><<<block_grid(p.Hk, blocks), kThreads, kSmem, st>>>(a));
-        if ((err = cudaGetLastError()) != cudaSuccess) return err;
+        MUIR_TIMED("k_attn_bwd", st,
+                   err = launch_early(k_attn_bwd<D>, p.q_rows > 0, block_grid(p.Hk, blocks), kThreads, kSmem, st, a));
+        if (err != cudaSuccess) return err;
     }
     return cudaSuccess;
 }

@@ -640,6 +640,7 @@ template <int D>
 __global__ void __launch_bounds__(D) k_attn_step_join(const float* part, const float* lse, __nv_bfloat16* o,
                                                       int splits) {
     __shared__ float w[kMaxSplits];
+    grid_wait();
     const long long head = blockIdx.x;
     const int ch = threadIdx.x;
     if (ch < splits) w[ch] = lse[head * splits + ch];
@@ -728,13 +729,12 @@ cudaError_t launch_attn_step(StepArgs a, int B, int d, void* ws, cudaStream_t st
     if (per == 8) err = d == 128 ? step<128, 1>(a, grid, st) : step<64, 1>(a, grid, st);
     else err = d == 128 ? step<128, 2>(a, grid, st) : step<64, 2>(a, grid, st);
     if (err != cudaSuccess || a.splits == 1) return err;
-    if (d == 128)
-        MUIR_TIMED("k_attn_step_join", st, k_attn_step_join<128><<<B * a.Hq, 128, 0, st>>>(
-            a.part, a.part_lse, static_cast<__nv_bfloat16*>(a.o), a.splits));
-    else
-        MUIR_TIMED("k_attn_step_join", st, k_attn_step_join<64><<<B * a.Hq, 64, 0, st>>>(
-            a.part, a.part_lse, static_cast<__nv_bfloat16*>(a.o), a.splits));
-    return cudaGetLastError();
+    __nv_bfloat16* o = static_cast<__nv_bfloat16*>(a.o);
+    const float *part = a.part, *lse = a.part_lse;
+    MUIR_TIMED("k_attn_step_join", st,
+               err = d == 128 ? launch_early(k_attn_step_join<128>, true, dim3(B * a.Hq), 128, 0, st, part, lse, o, a.splits)
+                              : launch_early(k_attn_step_join<64>, true, dim3(B * a.Hq), 64, 0, st, part, lse, o, a.splits));
+    return err;
 }
 
 unsigned int timeouts_kv() {

@@ -34,4 +34,29 @@ cudaError_t allow_smem(F* f, int bytes, std::atomic<uint64_t>& done) {
     return err;
 }
 
+// Launches `f`, with `early` so that its blocks may start while the kernel before it in the
+// stream (one of this library's own, launched in the same call) still runs: what they do
+// before grid_wait() must not touch what that kernel writes.
+template <class F, class... A>
+cudaError_t launch_early(F* f, bool early, dim3 grid, int threads, int smem, cudaStream_t st, const A&... args) {
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = (size_t)smem;
+    cfg.stream = st;
+    cfg.attrs = &attr;
+    cfg.numAttrs = early ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, f, args...);
+}
+
+#ifdef __CUDACC__
+// The kernel before (of launch_early) has finished and its writes are visible.
+__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+// Blocks of the kernel after may start.
+__device__ __forceinline__ void grid_release() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+#endif
+
 }  // namespace muir
