@@ -816,6 +816,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_bwd(const __grid_constant_
         if ((int)qblk < p.q_blocks)
             dq_block<D>(p, sm, (int)qblk, hk * p.group + (int)(i - qblk * per) * p.dq_heads, hk);
     }
+    grid_wait();  // blocks that needed no D: what follows in the stream may reuse its memory
 }
 
 template <int D>
@@ -901,6 +902,7 @@ cudaError_t run_bwd(const Problem& p, const void* o, const float* lse, const voi
                     void* dv, void* ws, cudaStream_t st) {
     BwdParams a;
     cudaError_t err = cudaSuccess;
+    if (p.q_rows == 0 && p.k_rows == 0) return err;
     if (p.q_rows > 0) {
         err = make_tmap_tokens(&a.tq, p.q, p.d, p.Hq, p.q_ld, p.q_rows, kTile);
         if (err == cudaSuccess)
