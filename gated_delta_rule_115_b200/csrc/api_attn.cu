@@ -10,9 +10,9 @@ namespace {
 
 bool aligned_to(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 bool ok_ints(const int* p) { return p != nullptr && aligned_to(p, 4); }
-bool ok_scale(float s) { return isfinite(s); }
 
 constexpr float kLog2e = 1.4426950408889634f;
+bool ok_scale(float s) { return isfinite(s * kLog2e); }  // as the kernels take it
 
 // Leading dimension of a token-major operand: 0 = dense; else a row's width at least,
 // and whole 16-byte vectors.
@@ -24,7 +24,7 @@ muir_status check_attn(const muir_attn_shape* s) {
     if (!s) return MUIR_ERR_INVALID_ARG;
     if (s->B < 0 || s->Tq < 0 || s->Tk < 0 || s->Hq <= 0 || s->Hk <= 0 || s->d <= 0 || s->window < 0)
         return MUIR_ERR_INVALID_ARG;
-    if (!(s->scale > 0.f) || !isfinite(s->scale) || s->Hq % s->Hk) return MUIR_ERR_INVALID_ARG;
+    if (!(s->scale > 0.f) || !ok_scale(s->scale) || s->Hq % s->Hk) return MUIR_ERR_INVALID_ARG;
     if (s->d != 64 && s->d != 128) return MUIR_ERR_UNSUPPORTED;
     const long long wq = (long long)s->Hq * s->d, wk = (long long)s->Hk * s->d;
     if (!ok_ld(s->q_ld, wq, 2) || !ok_ld(s->k_ld, wk, 2) || !ok_ld(s->v_ld, wk, 2)) return MUIR_ERR_INVALID_ARG;

@@ -201,3 +201,9 @@ def test_attention_workspace(m):
     assert m.lib().muir_attn_bwd_workspace(ctypes.byref(s)) == 2 * 100 * 4 * 8
     s.d = 32
     assert m.lib().muir_attn_bwd_workspace(ctypes.byref(s)) == 0
+
+
+def test_scales_that_leave_float32_in_base_two(m):
+    """The kernels take scale log2(e): past 2.35e38 that is no float32 any more."""
+    assert attn(m, scale=2.4e38) == attn(m, True, scale=2.4e38) == INVALID
+    assert step(m, cache(m), scale=2.4e38) == step(m, cache(m), scale=-2.4e38) == INVALID
