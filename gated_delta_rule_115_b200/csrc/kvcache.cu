@@ -157,7 +157,7 @@ __global__ void __launch_bounds__(NT) k_kv_append(AppendArgs p) {
     if (threadIdx.x == 0) *scale = now;
 
     const float inv = __frcp_rn(now);  // exact: a power of two in [2^-120, 2^100]
-    if (old > 0.f && now != old) {
+    if (now != old) {
         const float ratio = old / now;
         for (int i = threadIdx.x; i < held * (D / 4); i += NT) {
             uint32_t* w = reinterpret_cast<uint32_t*>(page) + i;

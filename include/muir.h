@@ -414,7 +414,8 @@ muir_status muir_rotary(int B, int T, int Hq, int Hk, int d, int rot, muir_dtype
  *   lse       : [B][Hq][Tq] float32
  * A query that sees no key gets o = 0, lse = -inf and no gradient; a key that no query
  * sees gets zero gradients.  Values of masked keys carry weight zero, not absence: a NaN
- * or an infinity there can reach queries of its own sequence; none reaches another one.
+ * or an infinity there (backward: in any row of q, k, v or dO) can reach other rows of its
+ * own sequence, padding included; none reaches another sequence.
  * Arithmetic: products of bfloat16 operands with float32 sums; softmax, lse and row sums
  * in float32; the weights, and in the backward pass their gradients, are rounded to
  * bfloat16 as operands of the second product.  Results repeat bit for bit: no atomics.
@@ -460,7 +461,7 @@ muir_status muir_attn_bwd_varlen(const muir_attn_shape* shape, int num_seqs,
  * A page holds `page` tokens (16, 32, 64 or 128) of all Hk key heads:
  *
  *   k_pages, v_pages : [num_pages][Hk][page][d] e4m3 codes
- *   k_scale, v_scale : [num_pages][Hk] float32; value = code * scale
+ *   k_scale, v_scale : [num_pages][Hk] float32, not negative; value = code * scale
  *   table            : device int32 [B][max_pages]; token t of sequence b lies in
  *                      page table[b][t / page], row t % page.  Entries outside
  *                      0 .. num_pages-1 name no page: nothing is written there,

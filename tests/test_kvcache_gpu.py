@@ -209,3 +209,48 @@ def test_step_in_a_graph_follows_lengths_and_cache(m):
         check(o, nq, [w[0] for w in want], [w[1] for w in want], table, at + 1)
         start += 1
         lens += 1
+
+
+def test_append_after_rows_of_scale_zero(m):
+    """A page that another writer filled with codes under scale 0 holds zeros, and still does
+    once new tokens give it a scale."""
+    Hk, page, d = 2, 32, 64
+    c = m.kv_cache(1, Hk, page, d)
+    for t in c[:2]:
+        t.view(torch.uint8).copy_(torch.arange(Hk * page * d, device="cuda").view(1, Hk, page, d) % 0x7f)
+    for t in c[2:]:
+        t.zero_()
+    x = torch.randn(1, 3, Hk, d, generator=torch.Generator().manual_seed(3)).cuda()
+    at = torch.tensor([5], dtype=torch.int32, device="cuda")
+    m.kv_append(x, x, *c, torch.zeros(1, 1, dtype=torch.int32, device="cuda"), at)
+    for i in range(2):
+        want, scale = A.kv_append(x.double().cpu().numpy(), np.zeros((1, Hk, page, d), np.uint8), np.zeros((1, Hk)),
+                                  np.zeros((1, 1), np.int64), [5], [3])
+        assert np.array_equal(c[2 + i].cpu().numpy(), scale)
+        assert np.array_equal(A.e4m3_decode(codes(c[i])[:, :, :8]), A.e4m3_decode(want[:, :, :8]))
+
+
+@pytest.mark.parametrize("lens", [[0, 0], [1, 0], [4096, 0], [4096, 4095]])
+def test_step_captured_twice(m, lens):
+    """Two graphs of the same step, each with its own output and parts, replayed in turn."""
+    code, scales, table, _ = filled(2, 4096, 2, 64, 128, 21, tail_nan=False)
+    g = torch.Generator().manual_seed(22)
+    qs = [torch.randn(2, 8, 64, generator=g).to(torch.bfloat16) for _ in range(2)]
+    ln = np.array(lens)
+    args = [x.cuda() for x in (torch.from_numpy(code[0]).view(torch.float8_e4m3fn),
+                               torch.from_numpy(code[1]).view(torch.float8_e4m3fn),
+                               torch.from_numpy(scales[0]).float(), torch.from_numpy(scales[1]).float(),
+                               torch.from_numpy(table), torch.from_numpy(ln.astype(np.int32)))]
+    outs, graphs, dq = [], [], [q.cuda() for q in qs]
+    m.attn_step(dq[0], *args)
+    for q in dq:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            outs.append(m.attn_step(q, *args))
+        graphs.append(graph)
+    for _ in range(3):
+        for graph in graphs:
+            graph.replay()
+    torch.cuda.synchronize()
+    for o, q in zip(outs, qs):
+        check(o, q, code, scales, table, ln)
