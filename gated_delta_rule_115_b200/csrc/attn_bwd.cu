@@ -410,7 +410,7 @@ __device__ __forceinline__ void dkv_block(const BwdParams& p, unsigned char* sm,
         const int wg = warp >> 2;
         const uint32_t lane0 = (uint32_t)(warp & 3) << 21;
         const int key = k0 + (threadIdx.x & 127);  // the thread's row
-        const bool all_single = p.window == 1 || sq.lk == 1;  // no query sees two keys
+        const bool all_single = (p.causal && p.window == 1) || sq.lk == 1;  // no query sees two keys
         const float c = p.scale_log2;
         bool ok = true;
         int tile = 0;  // of step j
@@ -426,8 +426,9 @@ __device__ __forceinline__ void dkv_block(const BwdParams& p, unsigned char* sm,
             const int sees = key - off - i0 - 64 * wg;
             const bool before = p.causal && i0 + off < k0 + kTile - 1;
             const bool behind = p.window && i0 + kTile - 1 + off - p.window >= k0;
-            // the column of a causal sequence's first position, whose query sees one key only
-            const int single = p.causal ? -off - i0 - 64 * wg : -1;
+            // the column whose query sees one key only: a causal sequence's first position, or the
+            // last one of those that look ahead from their own
+            const int single = p.causal ? -off - i0 - 64 * wg : p.window == 1 ? sq.lq - 1 - i0 - 64 * wg : -1;
             ok = warp_wait(bar->s_full + wg, j & 1) && warp_wait(bar->full + j % NS, (j / NS) & 1);
             if (!ok) break;
             tc_fence_after();

@@ -319,3 +319,22 @@ def test_rows_of_few_keys(m, T, window, Hq, Hk, d):
             tol = U * np.abs(r[n]) + (U + 2e-4) * r[n + "_abs"] + 2.0 ** -17 * r[n + "_dp"]
             within(g[n][b], r[n], tol, n)
     m.device_wait_status()
+
+
+@pytest.mark.parametrize("B,Tq,Tk,Hq,Hk,d,window", [
+    (1, 300, 300, 2, 1, 64, 1), (2, 300, 333, 2, 2, 128, 1), (1, 333, 200, 4, 2, 64, 1), (1, 129, 2, 2, 1, 128, 1),
+    (2, 200, 333, 4, 2, 64, 5), (1, 333, 200, 2, 1, 128, 8), (1, 140, 140, 8, 4, 64, 2)])
+def test_windows_that_look_ahead(m, B, Tq, Tk, Hq, Hk, d, window):
+    """Not causal, with a window: a query sees the last few keys up to its own and all
+    that follow; with a window of 1 the last query alone sees one key."""
+    q, k, v, do = (rnd(B, T, H, d, seed=s) for T, H, s in ((Tq, Hq, 1), (Tk, Hk, 2), (Tk, Hk, 3), (Tq, Hq, 4)))
+    rs = oracle(q, k, v, do, [(b, b) for b in range(B)], causal=False, window=window)
+    dev = [t.cuda() for t in (q, k, v, do)]
+    o, lse = m.attn_fwd(*dev[:3], causal=False, window=window)
+    g = m.attn_bwd(*dev[:3], o, lse, dev[3], causal=False, window=window)
+    m.device_wait_status()
+    for b, r in enumerate(rs):
+        check_fwd(o[b], lse[b], r)
+        check_bwd({n: t[b] for n, t in g.items()}, r, own_o=True)
+    if window == 1:
+        assert not g["dq"][:, -1].any()
