@@ -62,6 +62,7 @@ struct BwdParams {
 // as |v|): two visible keys leave 0.0038 in dq where everything else leaves 0.0023, sixteen
 // 0.0029.  Rows of up to kFewKeys keys take D = sum_j p_j dO . v_j instead, in float32.
 constexpr int kFewKeys = 8;
+constexpr int kDeltaRows = 4;  // of a lane, all in flight together
 
 struct DeltaParams {
     const __nv_bfloat16 *o, *dO, *q, *k, *v;
@@ -86,18 +87,20 @@ __device__ __forceinline__ int keys_seen(int causal, int window, int lk, int at)
     return max(0, last - first + 1);
 }
 
-__device__ __forceinline__ void unpack8(const __nv_bfloat16* p, float (&v)[8]) {
-    const uint4 u = *reinterpret_cast<const uint4*>(p);
+__device__ __forceinline__ void unpack8(const uint4& u, float (&v)[8]) {
     unpack16<true>(u.x, v[0], v[1]);
     unpack16<true>(u.y, v[2], v[3]);
     unpack16<true>(u.z, v[4], v[5]);
     unpack16<true>(u.w, v[6], v[7]);
 }
+__device__ __forceinline__ void unpack8(const __nv_bfloat16* p, float (&v)[8]) {
+    unpack8(*reinterpret_cast<const uint4*>(p), v);
+}
 
 // A row (token, head) of D channels is D / 8 lanes.  The first blocks take the rows of few
 // keys, beside the others, which read o and dO once and are bound by HBM.
 template <int D>
-__global__ void __launch_bounds__(256, 6) k_attn_delta(const __grid_constant__ DeltaParams p) {
+__global__ void __launch_bounds__(256, 4) k_attn_delta(const __grid_constant__ DeltaParams p) {
     constexpr int G = D / 8, RPW = 32 / G;
     if (p.release) grid_release();
     const int lane = threadIdx.x & 31, sub = (threadIdx.x >> 5) * RPW + lane / G, ch = (lane % G) * 8;
@@ -148,22 +151,33 @@ __global__ void __launch_bounds__(256, 6) k_attn_delta(const __grid_constant__ D
         if (few && lane % G == 0) p.few[out] = sum;
         return;
     }
-    const long long r = (long long)(blockIdx.x - p.few_blocks) * (8 * RPW) + sub;
-    float s = 0.f;
-    if (r < p.rows) {
-        float x[8], y[8];
-        unpack8(p.o + r * D + ch, x);
-        unpack8(p.dO + r * D + ch, y);
+    const long long r0 = (long long)(blockIdx.x - p.few_blocks) * (8 * RPW * kDeltaRows) + sub;
+    uint4 x[kDeltaRows], y[kDeltaRows];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) s += x[i] * y[i];
+    for (int n = 0; n < kDeltaRows; ++n) {
+        const long long r = r0 + n * 8 * RPW;
+        x[n] = y[n] = make_uint4(0u, 0u, 0u, 0u);
+        if (r < p.rows) {
+            x[n] = *reinterpret_cast<const uint4*>(p.o + r * D + ch);
+            y[n] = *reinterpret_cast<const uint4*>(p.dO + r * D + ch);
+        }
     }
-    s = row_sum(s);
-    if (r < p.rows && lane % G == 0) {
-        // token-major rows -> the layout of lse
-        const long long tok = r / p.Hq;
-        const int h = (int)(r - tok * p.Hq);
-        const long long b = p.lse_seq == 1 ? 0 : tok / p.T;
-        p.delta[b * p.T * p.lse_seq + h * p.lse_head + (tok - b * p.T)] = s;
+#pragma unroll
+    for (int n = 0; n < kDeltaRows; ++n) {
+        const long long r = r0 + n * 8 * RPW;
+        float a[8], b[8], s = 0.f;
+        unpack8(x[n], a);
+        unpack8(y[n], b);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) s += a[i] * b[i];
+        s = row_sum(s);
+        if (r < p.rows && lane % G == 0) {
+            // token-major rows -> the layout of lse
+            const long long tok = r / p.Hq;
+            const int h = (int)(r - tok * p.Hq);
+            const long long at = p.lse_seq == 1 ? 0 : tok / p.T;
+            p.delta[at * p.T * p.lse_seq + h * p.lse_head + (tok - at * p.T)] = s;
+        }
     }
 }
 
@@ -870,7 +884,7 @@ cudaError_t run(const Problem& p, BwdParams& a, const void* o, const void* dO, f
         }
         d.few_rows = (int)few_rows;
         d.few_blocks = (int)((few_rows * p.Hq + kRowsPerBlock - 1) / kRowsPerBlock);
-        const unsigned blocks = (unsigned)(d.few_blocks + (d.rows + kRowsPerBlock - 1) / kRowsPerBlock);
+        const unsigned blocks = (unsigned)(d.few_blocks + (d.rows + kRowsPerBlock * kDeltaRows - 1) / (kRowsPerBlock * kDeltaRows));
         if (blocks == 0) continue;
         MUIR_TIMED("k_attn_delta", st, k_attn_delta<D><<<blocks, 256, 0, st>>>(d));
         if ((err = cudaGetLastError()) != cudaSuccess) return err;

@@ -19,18 +19,6 @@ __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(saddr(bar)) : "memory");
 }
 
-// Whether the phase of parity `parity` has completed; never waits.
-__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
-    uint32_t done;
-    asm volatile(
-        "{\n.reg .pred p;\nmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n"
-        "selp.u32 %0, 1, 0, p;\n}"
-        : "=r"(done)
-        : "r"(saddr(bar)), "r"(parity)
-        : "memory");
-    return done != 0;
-}
-
 // kind::f16 with A read from tensor memory: lane m = row m, two 16-bit values a column.
 __device__ __forceinline__ void mma_f16_ta(uint32_t d, uint32_t a_tmem, uint64_t b, uint32_t id, uint32_t acc) {
     asm volatile(
@@ -55,60 +43,6 @@ __device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
     uint32_t r;
     asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
-}
-
-// Pairs of float32 in one 64-bit register: one instruction for both.
-__device__ __forceinline__ uint64_t pack2(float lo, float hi) {
-    uint64_t r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-    return r;
-}
-__device__ __forceinline__ void unpack2(uint64_t v, float& lo, float& hi) {
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-    uint64_t r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-    return r;
-}
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-    uint64_t r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-
-// Larger of two; NaN if either is.
-__device__ __forceinline__ float max_nan(float a, float b) {
-    float r;
-    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
-    return r;
-}
-
-// 2^x of a pair on the fused multiply-add units, for finite x <= 120 (x < -126 gives 2^-126):
-// x = n + f with n the nearest integer, 2^f by the polynomial that interpolates it at the
-// five Chebyshev nodes of [-1/2, 1/2] (relative error below 3.6e-6, its mean below 4e-8), n added to
-// the exponent.  The special-function units do 16 exponentials a clock and SM and are what
-// attention runs out of first; a share of them is moved here.
-__device__ __forceinline__ void ex2_poly2(uint64_t x, float& lo, float& hi) {
-    float a, b;
-    unpack2(x, a, b);
-    a = fmaxf(a, -126.f);
-    b = fmaxf(b, -126.f);
-    constexpr float kShift = 12582912.f;  // 1.5 2^23: adding it rounds to an integer
-    const uint64_t v = pack2(a, b);
-    const uint64_t t = add2(v, pack2(kShift, kShift));
-    const uint64_t n = add2(t, pack2(-kShift, -kShift));
-    const uint64_t f = fma2(n, pack2(-1.f, -1.f), v);
-    uint64_t p = pack2(0.00966636837f, 0.00966636837f);
-    p = fma2(p, f, pack2(0.0559219755f, 0.0559219755f));
-    p = fma2(p, f, pack2(0.240223497f, 0.240223497f));
-    p = fma2(p, f, pack2(0.693121016f, 0.693121016f));
-    p = fma2(p, f, pack2(1.f, 1.f));
-    float p0, p1, t0, t1;
-    unpack2(p, p0, p1);
-    unpack2(t, t0, t1);
-    lo = __uint_as_float(__float_as_uint(p0) + (__float_as_uint(t0) << 23));
-    hi = __uint_as_float(__float_as_uint(p1) + (__float_as_uint(t1) << 23));
 }
 
 // One tile of 128 tokens x D channels of one head: D / 64 boxes of 64 channels, 16 KB each.
