@@ -188,7 +188,7 @@ struct DkvSmem {
     static constexpr int kTileBytes = kTile * D * 2;
     static constexpr int kStages = D == 128 ? 2 : 4;                   // pairs of query and dO tiles
     static constexpr int kRing = 2 * kTileBytes;                       // after the two resident tiles
-    static constexpr int kVec = kRing + kStages * 2 * kTileBytes;      // -lse log2 e and D of a stage's rows
+    static constexpr int kVec = kRing + kStages * 2 * kTileBytes;      // -lse log2 e and -D of a stage's rows
     static constexpr int kBars = kVec + kStages * 2 * kTile * 4;
     static constexpr int kBytes = kBars + 512;
 };
@@ -319,7 +319,7 @@ __device__ __forceinline__ void dkv_block(const BwdParams& p, unsigned char* sm,
                 tile = 0;
                 ++head;
             }
-            // -lse log2 e and D of the tile's queries; -infinity (no weight at all) for rows
+            // -lse log2 e and -D of the tile's queries; -infinity (no weight at all) for rows
             // that do not exist and for queries that see no key; asked for before the stage is free
             const long long at = sq.q0 * p.lse_seq + h * p.lse_head + i0;
             const bool any_few = (p.window && p.window <= kFewKeys) || sq.lk <= kFewKeys ||
@@ -345,7 +345,7 @@ __device__ __forceinline__ void dkv_block(const BwdParams& p, unsigned char* sm,
                 // of one key or none: ds is zero, and D has not been formed
                 if (any_few && keys_seen(p.causal, p.window, sq.lk, i0 + x + off) <= 1) dd[n] = 0.f;
                 v[x] = e[n] == -INFINITY ? -INFINITY : -e[n] * kLog2e;
-                v[kTile + x] = dd[n];
+                v[kTile + x] = -dd[n];
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(bar->full + st);
@@ -425,7 +425,7 @@ __device__ __forceinline__ void dkv_block(const BwdParams& p, unsigned char* sm,
         const uint32_t lane0 = (uint32_t)(warp & 3) << 21;
         const int key = k0 + (threadIdx.x & 127);  // the thread's row
         const bool all_single = (p.causal && p.window == 1) || sq.lk == 1;  // no query sees two keys
-        const float c = p.scale_log2;
+        const uint64_t c2 = pack2(p.scale_log2, p.scale_log2);
         bool ok = true;
         int tile = 0;  // of step j
         for (int j = 0; j < steps && ok; ++j) {
@@ -463,10 +463,10 @@ __device__ __forceinline__ void dkv_block(const BwdParams& p, unsigned char* sm,
             for (int i = 0; i < 16; ++i) {
                 const float4 n = nl[i];
                 float* v = &s[i >> 3][(4 * i) & 31];
-                v[0] = ex2(fmaf(v[0], c, n.x));
-                v[1] = ex2(fmaf(v[1], c, n.y));
-                v[2] = ex2(fmaf(v[2], c, n.z));
-                v[3] = ex2(fmaf(v[3], c, n.w));
+                unpack2(fma2(pack2(v[0], v[1]), c2, pack2(n.x, n.y)), v[0], v[1]);
+                unpack2(fma2(pack2(v[2], v[3]), c2, pack2(n.z, n.w)), v[2], v[3]);
+#pragma unroll
+                for (int x = 0; x < 4; ++x) v[x] = ex2(v[x]);
             }
 #pragma unroll
             for (int i = 0; i < 32; ++i) w[i] = bf16x2(s[i >> 4][(2 * i) & 31], s[i >> 4][(2 * i + 1) & 31]);
@@ -499,10 +499,9 @@ __device__ __forceinline__ void dkv_block(const BwdParams& p, unsigned char* sm,
                 for (int i = 0; i < 8; ++i) {
                     const float4 n = dl[8 * hlf + i];
                     float* v = &s[hlf][4 * i];
-                    v[0] *= dp[4 * i] - n.x;
-                    v[1] *= dp[4 * i + 1] - n.y;
-                    v[2] *= dp[4 * i + 2] - n.z;
-                    v[3] *= dp[4 * i + 3] - n.w;
+                    unpack2(mul2(pack2(v[0], v[1]), add2(pack2(dp[4 * i], dp[4 * i + 1]), pack2(n.x, n.y))), v[0], v[1]);
+                    unpack2(mul2(pack2(v[2], v[3]), add2(pack2(dp[4 * i + 2], dp[4 * i + 3]), pack2(n.z, n.w))), v[2],
+                            v[3]);
                 }
 #pragma unroll
                 for (int i = 0; i < 16; ++i) w[16 * hlf + i] = bf16x2(s[hlf][2 * i], s[hlf][2 * i + 1]);
@@ -746,12 +745,13 @@ __device__ __forceinline__ void dq_block(const BwdParams& p, unsigned char* sm, 
                 if (e != -INFINITY) nls[n] = -e * kLog2e;
                 dls[n] = (seen <= kFewKeys ? p.few : p.delta)[v];
             }
-        const float c = p.scale_log2;
+        const uint64_t c2 = pack2(p.scale_log2, p.scale_log2);
         bool ok = true;
         for (int j = 0; j < steps && ok; ++j) {
             const uint32_t x = tmem + lane0 + (uint32_t)(j & 1) * 128u + 64u * wg;
             const int j0 = (lo + (j >> sh)) * kTile;
             const float nl = j & sh ? nls[1] : nls[0], dl = j & sh ? dls[1] : dls[0];
+            const uint64_t nl2 = pack2(nl, nl), dl2 = pack2(-dl, -dl);
             const int a = kmin - j0 - 64 * wg, b = kmax - j0 - 64 * wg;  // visible columns [a, b] of the 64
             ok = warp_wait(bar->s_full + 2 * wg + (j & 1), (j >> 1) & 1);
             if (!ok) break;
@@ -769,7 +769,12 @@ __device__ __forceinline__ void dq_block(const BwdParams& p, unsigned char* sm, 
                 for (int i = 0; i < 64; ++i) s[i >> 5][i & 31] = i >= a ? s[i >> 5][i & 31] : -INFINITY;
             }
 #pragma unroll
-            for (int i = 0; i < 64; ++i) s[i >> 5][i & 31] = ex2(fmaf(s[i >> 5][i & 31], c, nl));
+            for (int i = 0; i < 64; i += 2) {
+                float* v = &s[i >> 5][i & 31];
+                unpack2(fma2(pack2(v[0], v[1]), c2, nl2), v[0], v[1]);
+                v[0] = ex2(v[0]);
+                v[1] = ex2(v[1]);
+            }
             ok = warp_wait(bar->dp_full + wg, j & 1);
             if (!ok) break;
             tc_fence_after();
@@ -785,7 +790,10 @@ __device__ __forceinline__ void dq_block(const BwdParams& p, unsigned char* sm, 
                     if (lane == 0) mbar_arrive(bar->dp_read + wg);
                 }
 #pragma unroll
-                for (int i = 0; i < 32; ++i) s[hlf][i] *= dp[i] - dl;
+                for (int i = 0; i < 32; i += 2) {
+                    float* v = &s[hlf][i];
+                    unpack2(mul2(pack2(v[0], v[1]), add2(pack2(dp[i], dp[i + 1]), dl2)), v[0], v[1]);
+                }
 #pragma unroll
                 for (int i = 0; i < 16; ++i) w[16 * hlf + i] = bf16x2(s[hlf][2 * i], s[hlf][2 * i + 1]);
             }

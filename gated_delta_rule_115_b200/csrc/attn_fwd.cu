@@ -323,21 +323,26 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fwd(const __grid_constant_
                 }
             }
             const float neg = m == -INFINITY ? 0.f : -m;
-            float sum[4] = {0.f, 0.f, 0.f, 0.f};
+            const uint64_t c2 = pack2(c, c), neg2 = pack2(neg, neg);
+            uint64_t sum[2] = {0, 0};  // of even and odd columns, twice
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 uint32_t w[32];
 #pragma unroll
                 for (int x = 0; x < 32; ++x) {
-                    const float e0 = ex2(fmaf(s[2 * i + (x >> 4)][(2 * x) & 31], c, neg));
-                    const float e1 = ex2(fmaf(s[2 * i + (x >> 4)][(2 * x + 1) & 31], c, neg));
-                    sum[x & 1] += e0;
-                    sum[2 + (x & 1)] += e1;
+                    const float* v = &s[2 * i + (x >> 4)][(2 * x) & 31];
+                    float e0, e1;
+                    unpack2(fma2(pack2(v[0], v[1]), c2, neg2), e0, e1);
+                    e0 = ex2(e0);
+                    e1 = ex2(e1);
+                    sum[x & 1] = add2(sum[x & 1], pack2(e0, e1));
                     w[x] = bf16x2(e0, e1);
                 }
                 tmem_st32u(tP[t] + lane0 + 32 * i, w);
             }
-            l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+            float even, odd;
+            unpack2(add2(sum[0], sum[1]), even, odd);
+            l += even + odd;
             tmem_wait_st();
             tc_fence_before();
             __syncwarp();
