@@ -450,13 +450,10 @@ __device__ __forceinline__ void dkv_block(const BwdParams& p, unsigned char* sm,
             tmem_ld32(x, s[0]);
             tmem_ld32(x + 32, s[1]);
             tmem_wait_ld();
-            if (before) {
-#pragma unroll
-                for (int i = 0; i < 64; ++i) s[i >> 5][i & 31] = i >= sees ? s[i >> 5][i & 31] : -INFINITY;
-            }
-            if (behind) {
-#pragma unroll
-                for (int i = 0; i < 64; ++i) s[i >> 5][i & 31] = i < sees + p.window ? s[i >> 5][i & 31] : -INFINITY;
+            if (before || behind) {
+                const int a = p.causal ? sees : 0, b = p.window ? sees + p.window - 1 : 63;
+                hide(s[0], visible32(a, b));
+                hide(s[1], visible32(a - 32, b - 32));
             }
             uint32_t w[32];
 #pragma unroll
@@ -760,13 +757,9 @@ __device__ __forceinline__ void dq_block(const BwdParams& p, unsigned char* sm, 
             tmem_ld32(x, s[0]);
             tmem_ld32(x + 32, s[1]);
             tmem_wait_ld();
-            if (j0 + kTile - 1 > all_max) {
-#pragma unroll
-                for (int i = 0; i < 64; ++i) s[i >> 5][i & 31] = i <= b ? s[i >> 5][i & 31] : -INFINITY;
-            }
-            if (j0 < all_min) {
-#pragma unroll
-                for (int i = 0; i < 64; ++i) s[i >> 5][i & 31] = i >= a ? s[i >> 5][i & 31] : -INFINITY;
+            if (j0 + kTile - 1 > all_max || j0 < all_min) {
+                hide(s[0], visible32(a, b));
+                hide(s[1], visible32(a - 32, b - 32));
             }
 #pragma unroll
             for (int i = 0; i < 64; i += 2) {

@@ -71,6 +71,18 @@ __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
     return r;
 }
 
+// Columns 0 .. 31 of a row that columns [a, b] are visible of, a bit each.
+__device__ __forceinline__ uint32_t visible32(int a, int b) {
+    const uint32_t upto_b = b < 0 ? 0u : b >= 31 ? ~0u : (2u << b) - 1u;
+    const uint32_t below_a = a <= 0 ? 0u : a >= 32 ? ~0u : (1u << a) - 1u;
+    return upto_b & ~below_a;
+}
+// The others' scores become -infinity.
+__device__ __forceinline__ void hide(float (&s)[32], uint32_t visible) {
+#pragma unroll
+    for (int i = 0; i < 32; ++i) s[i] = visible & (1u << i) ? s[i] : -INFINITY;
+}
+
 // One tile of 128 tokens x D channels of one head: D / 64 boxes of 64 channels, 16 KB each.
 template <int D>
 __device__ __forceinline__ void load_tile(unsigned char* dst, const CUtensorMap* map, int head, int token,

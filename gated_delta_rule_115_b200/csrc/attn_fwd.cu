@@ -272,18 +272,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fwd(const __grid_constant_
             const int k0 = j * kTile;
             if (k0 + kTile - 1 > all_max || k0 < all_min) {
                 const int a = kmin - k0, b = kmax - k0;
-                if (k0 + kTile - 1 > all_max) {
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-#pragma unroll
-                        for (int x = 0; x < 32; ++x) s[i][x] = 32 * i + x <= b ? s[i][x] : -INFINITY;
-                }
-                if (k0 < all_min) {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-#pragma unroll
-                        for (int x = 0; x < 32; ++x) s[i][x] = 32 * i + x >= a ? s[i][x] : -INFINITY;
-                }
+                for (int i = 0; i < 4; ++i) hide(s[i], visible32(a - 32 * i, b - 32 * i));
             }
             float mx[4];
 #pragma unroll
