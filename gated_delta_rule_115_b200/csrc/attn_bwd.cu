@@ -227,7 +227,7 @@ __device__ __forceinline__ bool load_pair(unsigned char* dst, const CUtensorMap*
 
 template <int NS>
 struct DkvBars {
-    uint64_t res_full;                 // the resident tiles
+    uint64_t res_full, res_tmem;       // the resident tiles; in tensor memory too
     uint64_t full[NS], empty[NS], tail;
     // of each half of the columns:
     uint64_t s_full[2], dp_full[2];             // its products of a step in tensor memory
@@ -276,6 +276,7 @@ __device__ __forceinline__ void dkv_block(const BwdParams& p, unsigned char* sm,
     // meets: they take longer than everything else that comes before the first product.
     if (threadIdx.x == 32 * 11) {
         mbar_init(&bar->res_full, 1);
+        mbar_init(&bar->res_tmem, 8);
         for (int i = 0; i < NS; ++i) {
             mbar_init(bar->full + i, 2);
             mbar_init(bar->empty + i, 1);
@@ -304,6 +305,12 @@ __device__ __forceinline__ void dkv_block(const BwdParams& p, unsigned char* sm,
     tc_fence_after();
     const uint32_t tmem = bar->tmem_slot;
     const uint32_t tV = tmem + 256u, tK = tmem + 256u + (uint32_t)D;
+    // At D = 64 there is room for the resident tiles beside the sums, K in 32 columns and V in the
+    // next: as operands they are then no part of what the products fetch from shared memory,
+    // which for 64 columns a product is more than the tensor cores keep up with (8192 tokens, 8
+    // heads: 254 -> 250 us; 8 over 2: 312 -> 300).
+    constexpr bool RES = D == 64;
+    const uint32_t tRes = tmem + 384u;
     float* vec = reinterpret_cast<float*>(sm + SM::kVec);
 
     if (warp == 11) {
@@ -358,7 +365,7 @@ __device__ __forceinline__ void dkv_block(const BwdParams& p, unsigned char* sm,
         bool ok = true;
         if (lane != 0 || steps == 0) {
         } else if (warp == 8) {  // S = K Q^T
-            ok = mbar_wait(&bar->res_full, 0);
+            ok = mbar_wait(RES ? &bar->res_tmem : &bar->res_full, 0);
             const uint32_t a = saddr(sm);
             for (int j = 0; j < steps && ok; ++j) {
                 const uint32_t b = saddr(sm + SM::kRing + (j % NS) * 2 * SM::kTileBytes);
@@ -371,12 +378,13 @@ __device__ __forceinline__ void dkv_block(const BwdParams& p, unsigned char* sm,
                     const uint32_t d = tmem + 128u * u + (uint32_t)(j & 1) * 64u;
 #pragma unroll
                     for (int k = 0; k < D; k += 16)
-                        mma_f16(d, kdesc16(a, 0, k), kdesc16(b, 64 * u, k), id_s, k ? 1u : 0u);
+                        if (RES) mma_f16_ta(d, tRes + k / 2, kdesc16(b, 64 * u, k), id_s, k ? 1u : 0u);
+                        else mma_f16(d, kdesc16(a, 0, k), kdesc16(b, 64 * u, k), id_s, k ? 1u : 0u);
                     mma_commit(bar->s_full + u);
                 }
             }
         } else if (warp == 9) {  // P = V dO^T, where the step before kept p and ds
-            ok = mbar_wait(&bar->res_full, 0);
+            ok = mbar_wait(RES ? &bar->res_tmem : &bar->res_full, 0);
             const uint32_t a = saddr(sm + SM::kTileBytes);
             for (int j = 0; j < steps && ok; ++j) {
                 const uint32_t b = saddr(sm + SM::kRing + (j % NS) * 2 * SM::kTileBytes + SM::kTileBytes);
@@ -389,7 +397,8 @@ __device__ __forceinline__ void dkv_block(const BwdParams& p, unsigned char* sm,
                     const uint32_t d = tmem + 128u * u + (uint32_t)(1 - (j & 1)) * 64u;
 #pragma unroll
                     for (int k = 0; k < D; k += 16)
-                        mma_f16(d, kdesc16(a, 0, k), kdesc16(b, 64 * u, k), id_s, k ? 1u : 0u);
+                        if (RES) mma_f16_ta(d, tRes + 32 + k / 2, kdesc16(b, 64 * u, k), id_s, k ? 1u : 0u);
+                        else mma_f16(d, kdesc16(a, 0, k), kdesc16(b, 64 * u, k), id_s, k ? 1u : 0u);
                     mma_commit(bar->dp_full + u);
                 }
             }
@@ -427,6 +436,24 @@ __device__ __forceinline__ void dkv_block(const BwdParams& p, unsigned char* sm,
         const bool all_single = (p.causal && p.window == 1) || sq.lk == 1;  // no query sees two keys
         const uint64_t c2 = pack2(p.scale_log2, p.scale_log2);
         bool ok = true;
+        if (RES && steps > 0) {
+            ok = warp_wait(&bar->res_full, 0);
+            const unsigned char* from = sm + wg * SM::kTileBytes;
+            uint32_t w[32];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const uint4 v = *reinterpret_cast<const uint4*>(from + t16_off(threadIdx.x & 127, i));
+                w[4 * i] = v.x;
+                w[4 * i + 1] = v.y;
+                w[4 * i + 2] = v.z;
+                w[4 * i + 3] = v.w;
+            }
+            tmem_st32u(tRes + lane0 + 32u * wg, w);
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bar->res_tmem);
+        }
         int tile = 0;  // of step j
         for (int j = 0; j < steps && ok; ++j) {
             const uint32_t x = tmem + lane0 + 128u * wg + (uint32_t)(j & 1) * 64u;
