@@ -22,7 +22,9 @@
 // the product's operands; the sums are of the unrounded ones, in float32.
 //
 // Bound by the tensor cores (4 d flops a visible pair) and, at d = 64 before anything else,
-// by the exponentials (16 a clock and SM).
+// by the exponentials (16 a clock and SM).  Causal, 16384 tokens of 16 heads over 4 of 128: 0.80
+// ms, 1.37 PFLOP/s, in short runs; 0.93 ms, 1.18, once the power limit sets the clock.  8192 tokens
+// of 8 heads of 64: 104 us, 0.66 PFLOP/s.
 #include <algorithm>
 
 #include "attn_dev.cuh"
