@@ -71,7 +71,7 @@ __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
     return r;
 }
 
-// Columns 0 .. 31 of a row that columns [a, b] are visible of, a bit each.
+// A bit for each of columns 0 .. 31: those in [a, b].
 __device__ __forceinline__ uint32_t visible32(int a, int b) {
     const uint32_t upto_b = b < 0 ? 0u : b >= 31 ? ~0u : (2u << b) - 1u;
     const uint32_t below_a = a <= 0 ? 0u : a >= 32 ? ~0u : (1u << a) - 1u;
