@@ -26,7 +26,7 @@ __all__ = [
     "MuirError", "lib", "chunk_fwd", "chunk_bwd", "chunk_fwd_varlen", "chunk_bwd_varlen",
     "recurrent_step", "qk_prologue", "chunk_fwd_fused", "chunk_bwd_fused", "MuirFusion",
     "qk_prologue_bwd", "rotary", "rotary_frequencies", "attn_fwd", "attn_bwd",
-    "attn_fwd_varlen", "attn_bwd_varlen", "MuirAttentionFunction", "kv_cache", "kv_append", "attn_step",
+    "attn_fwd_varlen", "attn_bwd_varlen", "MuirRotaryFunction", "MuirAttentionFunction", "kv_cache", "kv_append", "attn_step",
     "fwd_workspace_bytes", "bwd_workspace_bytes", "MuirChunkFunction",
     "LIB_PATH",
 ]
@@ -562,7 +562,8 @@ def rotary(q, k=None, positions=None, inv_freq=None, interleaved=False, mscale=1
     ``[rot / 2]`` (see :func:`rotary_frequencies`) and fixes the rotated channels.
     ``inverse`` applies the transpose, which maps an output gradient to the input's.
     ``q_out`` / ``k_out`` may be the inputs (in place).  Returns ``(q_out, k_out)``, or
-    ``q_out`` alone without ``k``."""
+    ``q_out`` alone without ``k``.  Records nothing with autograd, and refuses tensors that
+    require a gradient while gradients are enabled: :class:`MuirRotaryFunction` takes those."""
     return (_nat or _native()).rotary(q, k, positions, inv_freq, interleaved, mscale, inverse, q_out, k_out)
 
 
@@ -639,6 +640,44 @@ class MuirChunkFunction(torch.autograd.Function):
                        chunk=ctx.chunk, S_chunks=Sc, M_chunks=Mc, aux=aux)
         return (gr["dq"], gr["dk"], gr["dv"], gr["dg"], gr["de"], gr["dw"], gr["dgamma"],
                 gr["dS0"] if S0 is not None else None, None)
+
+
+class MuirRotaryFunction(torch.autograd.Function):
+    """Autograd wrapper of :func:`rotary`: ``apply(q, k, positions, inv_freq, interleaved,
+    mscale, inverse, inplace)`` returns what it does.  The map is linear: its gradient is the
+    call with ``inverse`` turned over, and differentiable in its turn.
+
+    ``inplace`` writes over ``q`` and ``k``.  Autograd takes neither leaves for that, nor views
+    in a call that returns two tensors: parts of one projection are rotated in a call each."""
+
+    @staticmethod
+    def forward(ctx, q, k=None, positions=None, inv_freq=None, interleaved=False, mscale=1.0, inverse=False,
+                inplace=False):
+        ctx.set_materialize_grads(False)
+        ctx.args = (interleaved, mscale, not inverse)
+        ctx.save_for_backward(positions, inv_freq)
+        if not inplace:
+            return rotary(q, k, positions, inv_freq, interleaved, mscale, inverse)
+        both = (q,) if k is None else (q, k)
+        if any(ctx.needs_input_grad[:2]):  # what autograd itself refuses, before anything is written
+            if any(t.is_leaf and t.requires_grad for t in both):
+                raise ValueError("a leaf that requires a gradient cannot be rotated in place")
+            if len(both) > 1 and any(t._is_view() for t in both):
+                raise ValueError("views of a larger tensor are rotated in place in a call each")
+        ctx.mark_dirty(*both)
+        rotary(q, k, positions, inv_freq, interleaved, mscale, inverse, q_out=q, k_out=k)
+        return q if k is None else both
+
+    @staticmethod
+    def backward(ctx, *grads):
+        rest = *ctx.saved_tensors, *ctx.args
+        had = [g.contiguous() for g in grads if g is not None]
+        if len(had) == 2:
+            d = MuirRotaryFunction.apply(*had, *rest)
+        else:
+            one = MuirRotaryFunction.apply(had[0], None, *rest) if had else None
+            d = [None if g is None else one for g in (*grads, None)[:2]]
+        return (*d, None, None, None, None, None, None)
 
 
 class MuirAttentionFunction(torch.autograd.Function):

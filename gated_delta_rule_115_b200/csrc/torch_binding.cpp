@@ -9,6 +9,7 @@
 #include <dlfcn.h>
 #include <torch/extension.h>
 
+#include <cmath>
 #include <optional>
 #include <string>
 #include <vector>
@@ -132,9 +133,20 @@ Tensor workspace(size_t bytes, const OptTensor& ws, c10::Device dev) {
 
 // ------------------------------------------------------------------ rotary
 
+bool tracked(const Tensor& t) { return t.requires_grad() && at::GradMode::is_enabled(); }
+bool tracked(const OptTensor& t) { return t && tracked(*t); }
+
+// A tensor of the caller's was written: autograd's check of what it saved has to see it.
+void written(const OptTensor& t) {
+    if (t && !t->is_inference()) t->unsafeGetTensorImpl()->bump_version();
+}
+
 py::object rotary(const Tensor& q, const OptTensor& k, const OptTensor& positions, const OptTensor& inv_freq,
                   bool interleaved, double mscale, bool inverse, const OptTensor& q_out, const OptTensor& k_out) {
     if (!inv_freq) bad("inv_freq is required (rotary_frequencies makes it)");
+    if (tracked(q) || tracked(k) || tracked(q_out) || tracked(k_out))
+        bad("rotary records no gradient and would cut or falsify it: call MuirRotaryFunction.apply, or rotary "
+            "under torch.no_grad()");
     const muir_dtype dt = dtype_of(q);
     const c10::Device dev = q.device();
     const Rows rq = rows(q, "q", dev);
@@ -160,6 +172,8 @@ py::object rotary(const Tensor& q, const OptTensor& k, const OptTensor& position
                      as_int(d, "d"), as_int(2 * half, "rot"), dt, rq.p, rq.ld, rk.p, rk.ld,
                      static_cast<const int*>(pos), static_cast<const double*>(freq), (float)mscale, interleaved,
                      inverse, wq.p, wq.ld, wk.p, wk.ld, c.stream));
+    written(q_out);
+    written(k_out);
     if (!k) return py::cast(oq);
     return py::make_tuple(oq, ok);
 }
