@@ -18,6 +18,7 @@ from __future__ import annotations
 
 import ctypes
 import math
+import operator
 import os
 
 import torch
@@ -582,6 +583,13 @@ def attn_bwd(q, k, v, o, lse, dO, causal=True, window=0, scale=None, ws=None):
     return (_nat or _native()).attn_bwd(q, k, v, o, lse, dO, None, None, causal, window, scale, ws)
 
 
+def _offsets(cu):
+    """A copy of host offsets (a list or a tensor), None kept."""
+    if cu is None:
+        return None
+    return tuple(cu.to("cpu", torch.long).tolist() if torch.is_tensor(cu) else map(operator.index, cu))
+
+
 def attn_fwd_varlen(q, k, v, cu_seqlens, cu_seqlens_k=None, causal=True, window=0, scale=None):
     """:func:`attn_fwd` over packed sequences: ``q [1, T, Hq, d]``, ``k, v [1, Tk, Hk, d]`` with
     sequence i at rows ``cu_seqlens[i]:cu_seqlens[i+1]`` (a host list or CPU tensor;
@@ -682,12 +690,14 @@ class MuirRotaryFunction(torch.autograd.Function):
 
 class MuirAttentionFunction(torch.autograd.Function):
     """Autograd wrapper of :func:`attn_fwd` / :func:`attn_bwd`, or of the varlen forms with
-    ``cu_seqlens``; returns ``o``."""
+    ``cu_seqlens``, which is copied: its owner may refill it before the backward pass.
+    Returns ``o``."""
 
     @staticmethod
     def forward(ctx, q, k, v, causal=True, window=0, scale=None, cu_seqlens=None, cu_seqlens_k=None):
         ctx.args = dict(causal=causal, window=window, scale=scale)
-        ctx.cu = None if cu_seqlens is None else dict(cu_seqlens=cu_seqlens, cu_seqlens_k=cu_seqlens_k)
+        ctx.cu = (None if cu_seqlens is None
+                  else dict(cu_seqlens=_offsets(cu_seqlens), cu_seqlens_k=_offsets(cu_seqlens_k)))
         o, lse = (attn_fwd(q, k, v, **ctx.args) if ctx.cu is None
                   else attn_fwd_varlen(q, k, v, **ctx.cu, **ctx.args))
         ctx.save_for_backward(q, k, v, o, lse)

@@ -104,7 +104,62 @@ def test_rotary_in_place_on_parts_of_a_projection(m, monkeypatch):
     assert torch.allclose(leaf.grad, want.grad, rtol=1e-12)
 
 
-# ------------------------------------------------------------------ rotary, on the GPU
+# ------------------------------------------------------------------ attention, on the CPU
+
+
+def plain_attention(q, k, v, causal, window, scale, cu=None, cu_k=None):
+    """Float64 attention of packed (or dense) sequences, in torch."""
+    cu = [0, q.shape[1]] if cu is None else [int(x) for x in cu]
+    cu_k = ([0, k.shape[1]] if cu == [0, q.shape[1]] else cu) if cu_k is None else [int(x) for x in cu_k]
+    o = []
+    for a, b, c, d in zip(cu, cu[1:], cu_k, cu_k[1:]):
+        see = torch.tensor(A.visible(b - a, d - c, causal, window))
+        kk, vv = (t[:, c:d].repeat_interleave(q.shape[2] // k.shape[2], 2) for t in (k, v))
+        z = torch.einsum("bihd,bjhd->bhij", q[:, a:b], kk) * (q.shape[-1] ** -0.5 if scale is None else scale)
+        p = torch.softmax(z.masked_fill(~see, -1e300), -1) * see.any(1)[:, None]
+        o.append(torch.einsum("bhij,bjhd->bihd", p, vv))
+    return torch.cat(o, 1)
+
+
+@pytest.fixture
+def plain(m, monkeypatch):
+    """The module with its attention calls replaced by float64 formulas on the CPU."""
+    def fwd(q, k, v, cu=None, cu_k=None, causal=True, window=0, scale=None):
+        return plain_attention(q, k, v, causal, window, scale, cu, cu_k), torch.zeros(1)
+
+    def bwd(q, k, v, o, lse, dO, cu=None, cu_k=None, causal=True, window=0, scale=None, ws=None):
+        with torch.enable_grad():
+            x = [t.detach().double().requires_grad_() for t in (q, k, v)]
+            g = torch.autograd.grad(plain_attention(*x, causal, window, scale, cu, cu_k), x, dO.double())
+        return dict(zip(("dq", "dk", "dv"), g))
+
+    monkeypatch.setattr(m, "attn_fwd", lambda q, k, v, **kw: fwd(q, k, v, **kw))
+    monkeypatch.setattr(m, "attn_bwd", lambda q, k, v, o, lse, dO, **kw: bwd(q, k, v, o, lse, dO, **kw))
+    monkeypatch.setattr(m, "attn_fwd_varlen", lambda q, k, v, cu_seqlens, cu_seqlens_k=None, **kw:
+                        fwd(q, k, v, cu_seqlens, cu_seqlens_k, **kw))
+    monkeypatch.setattr(m, "attn_bwd_varlen", lambda q, k, v, o, lse, dO, cu_seqlens, cu_seqlens_k=None, **kw:
+                        bwd(q, k, v, o, lse, dO, cu_seqlens, cu_seqlens_k, **kw))
+    return m
+
+
+@pytest.mark.parametrize("kind", [list, torch.tensor, np.array])
+@pytest.mark.parametrize("apart", [False, True])
+def test_offsets_refilled_before_the_backward_pass(plain, kind, apart):
+    """The gradients belong to the sequences of the forward pass, whatever the caller's
+    buffer of offsets holds by then.  (The wrapper rounds dO to bfloat16: ones are exact.)"""
+    q, k, v = (rnd(1, 12, H, 8, seed=H, dtype=torch.float64) for H in (4, 2, 2))
+    cu, ck = [0, 5, 12], [0, 9, 12]
+    held, held_k = kind(cu), kind(ck)
+    got, want = ([t.clone().requires_grad_() for t in (q, k, v)] for _ in range(2))
+    o = plain.MuirAttentionFunction.apply(*got, True, 0, None, held, held_k if apart else None)
+    held[1], held_k[1] = 7, 2
+    o.sum().backward()
+    plain_attention(*want, True, 0, None, cu, ck if apart else None).sum().backward()
+    for a, b in zip(got, want):
+        assert torch.allclose(a.grad, b.grad, rtol=1e-12, atol=1e-13)
+
+
+# ------------------------------------------------------------------ on the GPU
 
 
 @pytest.mark.gpu
@@ -168,3 +223,16 @@ def test_rotary_in_place_is_seen_by_saved_tensors(m):
         want = m.rotary(z, inv_freq=f)
         m.rotary(z, inv_freq=f, q_out=z)
         assert torch.equal(z, want)
+
+
+@pytest.mark.gpu
+def test_offsets_refilled_before_the_backward_pass_of_the_kernels(m):
+    q, k, v, do = (rnd(1, 400, H, 64, seed=s).cuda() for H, s in ((4, 1), (2, 2), (2, 3), (4, 4)))
+    cu = torch.tensor([0, 130, 400])
+    leaves = [t.clone().requires_grad_() for t in (q, k, v)]
+    o = m.MuirAttentionFunction.apply(*leaves, True, 0, None, cu)
+    cu[1] = 255
+    o.backward(do)
+    g = m.attn_bwd_varlen(q, k, v, *m.attn_fwd_varlen(q, k, v, [0, 130, 400]), do, [0, 130, 400])
+    assert all(torch.equal(t.grad, g[n]) for t, n in zip(leaves, ("dq", "dk", "dv")))
+    m.device_wait_status()
