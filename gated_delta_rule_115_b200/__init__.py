@@ -590,18 +590,25 @@ def _offsets(cu):
     return tuple(cu.to("cpu", torch.long).tolist() if torch.is_tensor(cu) else map(operator.index, cu))
 
 
+def _given(cu):
+    """The native calls take None for a dense batch: packed rows would run as one sequence."""
+    if cu is None:
+        raise ValueError("packed sequences need cu_seqlens")
+    return cu
+
+
 def attn_fwd_varlen(q, k, v, cu_seqlens, cu_seqlens_k=None, causal=True, window=0, scale=None):
     """:func:`attn_fwd` over packed sequences: ``q [1, T, Hq, d]``, ``k, v [1, Tk, Hk, d]`` with
     sequence i at rows ``cu_seqlens[i]:cu_seqlens[i+1]`` (a host list or CPU tensor;
     ``cu_seqlens_k`` for the keys where they differ).  ``lse`` is ``[1, Hq, T]``."""
-    return (_nat or _native()).attn_fwd(q, k, v, cu_seqlens, cu_seqlens_k, causal, window, scale)
+    return (_nat or _native()).attn_fwd(q, k, v, _given(cu_seqlens), cu_seqlens_k, causal, window, scale)
 
 
 def attn_bwd_varlen(q, k, v, o, lse, dO, cu_seqlens, cu_seqlens_k=None, causal=True, window=0,
                     scale=None, ws=None):
     """Gradients through :func:`attn_fwd_varlen`; returns the dict of :func:`attn_bwd`."""
-    return (_nat or _native()).attn_bwd(q, k, v, o, lse, dO, cu_seqlens, cu_seqlens_k, causal, window,
-                                        scale, ws)
+    return (_nat or _native()).attn_bwd(q, k, v, o, lse, dO, _given(cu_seqlens), cu_seqlens_k, causal,
+                                        window, scale, ws)
 
 
 def kv_cache(num_pages, Hk, page, d, device="cuda"):
@@ -696,7 +703,7 @@ class MuirAttentionFunction(torch.autograd.Function):
     @staticmethod
     def forward(ctx, q, k, v, causal=True, window=0, scale=None, cu_seqlens=None, cu_seqlens_k=None):
         ctx.args = dict(causal=causal, window=window, scale=scale)
-        ctx.cu = (None if cu_seqlens is None
+        ctx.cu = (None if cu_seqlens is None and cu_seqlens_k is None
                   else dict(cu_seqlens=_offsets(cu_seqlens), cu_seqlens_k=_offsets(cu_seqlens_k)))
         o, lse = (attn_fwd(q, k, v, **ctx.args) if ctx.cu is None
                   else attn_fwd_varlen(q, k, v, **ctx.cu, **ctx.args))

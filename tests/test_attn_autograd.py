@@ -159,6 +159,17 @@ def test_offsets_refilled_before_the_backward_pass(plain, kind, apart):
         assert torch.allclose(a.grad, b.grad, rtol=1e-12, atol=1e-13)
 
 
+def test_key_offsets_alone_are_refused(m):
+    """Packed rows must not run as one dense sequence."""
+    q, lse = torch.zeros(1, 6, 2, 64, dtype=torch.bfloat16), torch.zeros(1, 2, 6)
+    ck = [0, 2, 6]
+    for call in (lambda: m.attn_fwd_varlen(q, q, q, None), lambda: m.attn_fwd_varlen(q, q, q, None, ck),
+                 lambda: m.attn_bwd_varlen(q, q, q, q, lse, q, None), lambda: m.attn_bwd_varlen(q, q, q, q, lse, q, None, ck),
+                 lambda: m.MuirAttentionFunction.apply(q, q, q, True, 0, None, None, ck)):
+        with pytest.raises(ValueError, match="cu_seqlens"):
+            call()
+
+
 # ------------------------------------------------------------------ on the GPU
 
 
