@@ -636,6 +636,22 @@ def attn_step(q, k_pages, v_pages, k_scale, v_scale, page_table, lens, scale=Non
                                          window, o, ws)
 
 
+class _Once(torch.autograd.Function):
+    """``apply(n, *tensors)``: the first n, gradients without a derivative of their own, as results
+    of the others, which they were formed from.  Differentiating them again raises, where it
+    would leave that part out (with ``once_differentiable`` it still would, wherever the
+    incoming gradient is a constant: that looks at the arguments, not at what was saved)."""
+
+    @staticmethod
+    def forward(ctx, n, *tensors):
+        return tuple(None if t is None else t.view_as(t) for t in tensors[:n])
+
+    @staticmethod
+    def backward(ctx, *grads):
+        raise RuntimeError("this backward pass is a kernel without a derivative: its gradients cannot be "
+                           "differentiated again")
+
+
 class MuirChunkFunction(torch.autograd.Function):
     """Autograd wrapper: forward saves the chunk states, backward reuses them."""
 
@@ -653,8 +669,11 @@ class MuirChunkFunction(torch.autograd.Function):
         gr = chunk_bwd(q, k, v, g, e, w, gamma, S0, dO.contiguous().to(q.dtype),
                        None if dS_final is None else dS_final.contiguous().float(),
                        chunk=ctx.chunk, S_chunks=Sc, M_chunks=Mc, aux=aux)
-        return (gr["dq"], gr["dk"], gr["dv"], gr["dg"], gr["de"], gr["dw"], gr["dgamma"],
-                gr["dS0"] if S0 is not None else None, None)
+        out = (gr["dq"], gr["dk"], gr["dv"], gr["dg"], gr["de"], gr["dw"], gr["dgamma"],
+               gr["dS0"] if S0 is not None else None)
+        if torch.is_grad_enabled():  # create_graph
+            out = _Once.apply(len(out), *out, q, k, v, g, e, w, gamma, S0, dO, dS_final)
+        return *out, None
 
 
 class MuirRotaryFunction(torch.autograd.Function):
@@ -716,4 +735,7 @@ class MuirAttentionFunction(torch.autograd.Function):
         dO = dO.contiguous().to(torch.bfloat16)
         g = (attn_bwd(*saved, dO, **ctx.args) if ctx.cu is None
              else attn_bwd_varlen(*saved, dO, **ctx.cu, **ctx.args))
-        return g["dq"], g["dk"], g["dv"], None, None, None, None, None
+        out = g["dq"], g["dk"], g["dv"]
+        if torch.is_grad_enabled():  # create_graph
+            out = _Once.apply(len(out), *out, *saved[:3], dO)
+        return *out, None, None, None, None, None

@@ -131,7 +131,7 @@ def plain(m, monkeypatch):
         with torch.enable_grad():
             x = [t.detach().double().requires_grad_() for t in (q, k, v)]
             g = torch.autograd.grad(plain_attention(*x, causal, window, scale, cu, cu_k), x, dO.double())
-        return dict(zip(("dq", "dk", "dv"), g))
+        return dict(zip(("dq", "dk", "dv"), (t.detach() for t in g)))
 
     monkeypatch.setattr(m, "attn_fwd", lambda q, k, v, **kw: fwd(q, k, v, **kw))
     monkeypatch.setattr(m, "attn_bwd", lambda q, k, v, o, lse, dO, **kw: bwd(q, k, v, o, lse, dO, **kw))
@@ -157,6 +157,39 @@ def test_offsets_refilled_before_the_backward_pass(plain, kind, apart):
     plain_attention(*want, True, 0, None, cu, ck if apart else None).sum().backward()
     for a, b in zip(got, want):
         assert torch.allclose(a.grad, b.grad, rtol=1e-12, atol=1e-13)
+
+
+def chunk_stand_in(m, monkeypatch):
+    """MuirChunkFunction over a formula that is quadratic in q (its second gradient is not 0)."""
+    def fwd(q, k, v, g, e, w, gamma, S0=None, **kw):
+        return q * q * v, torch.zeros(1), None, None, None
+
+    def bwd(q, k, v, g, e, w, gamma, S0, dO, dS, **kw):
+        z = torch.zeros_like(q)
+        return dict(dq=2 * q * v * dO, dk=z, dv=q * q * dO, dg=z, de=z, dw=z, dgamma=z, dS0=None)
+
+    monkeypatch.setattr(m, "chunk_fwd", fwd)
+    monkeypatch.setattr(m, "chunk_bwd", bwd)
+
+
+@pytest.mark.parametrize("which", ["attention", "chunk"])
+def test_gradients_of_gradients_are_refused(plain, monkeypatch, which):
+    """The backward passes have no derivative of their own: a gradient penalty has to fail
+    where it is taken, not vanish.  The first gradient with create_graph stays as it was."""
+    x = [rnd(1, 6, 2, 8, seed=s, dtype=torch.float64).requires_grad_() for s in range(7)]
+    if which == "attention":
+        o = plain.MuirAttentionFunction.apply(*x[:3])
+        want = torch.autograd.grad(plain_attention(*x[:3], True, 0, None).sum(), x[0])
+    else:
+        chunk_stand_in(plain, monkeypatch)
+        o, _ = plain.MuirChunkFunction.apply(*x, None, 64)
+        want = (2 * x[0] * x[2],)
+    # the loss holds q by another path as well, which a silently dropped part would leave
+    loss = o.sum() + (x[0] ** 2).sum()
+    got = torch.autograd.grad(loss, x[0], create_graph=True)
+    assert torch.allclose(got[0], want[0] + 2 * x[0], rtol=1e-12)
+    with pytest.raises(RuntimeError, match="differentiated again"):
+        (got[0] ** 2).sum().backward()
 
 
 def test_key_offsets_alone_are_refused(m):
@@ -246,4 +279,31 @@ def test_offsets_refilled_before_the_backward_pass_of_the_kernels(m):
     o.backward(do)
     g = m.attn_bwd_varlen(q, k, v, *m.attn_fwd_varlen(q, k, v, [0, 130, 400]), do, [0, 130, 400])
     assert all(torch.equal(t.grad, g[n]) for t, n in zip(leaves, ("dq", "dk", "dv")))
+    m.device_wait_status()
+
+
+@pytest.mark.gpu
+def test_gradients_with_create_graph(m):
+    """The same gradients as without, and no second ones."""
+    q, k, v = (rnd(1, 130, H, 64, seed=s).cuda().requires_grad_() for H, s in ((4, 1), (2, 2), (2, 3)))
+    first = torch.autograd.grad(m.MuirAttentionFunction.apply(q, k, v).float().sum(), (q, k, v))
+    again = torch.autograd.grad(m.MuirAttentionFunction.apply(q, k, v).float().sum(), (q, k, v), create_graph=True)
+    assert all(torch.equal(a, b) for a, b in zip(first, again))
+    with pytest.raises(RuntimeError, match="differentiated again"):
+        sum((t.float() ** 2).sum() for t in again).backward()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("state", [False, True])
+def test_chunk_gradients_with_create_graph(m, state):
+    from gated_delta_rule_115_b200.inputs import chunk_inputs
+    x = chunk_inputs(0, B=1, H=2, T=150)
+    x = [None if t is None else t.cuda() for t in (x[n] for n in ("q", "k", "v", "g", "e", "w", "gamma", "S0"))]
+    x[7] = torch.randn(1, 2, *x[0].shape[-1:], x[2].shape[-1], device="cuda") if state else None
+    leaves = [t.requires_grad_() for t in x if t is not None]
+    got = [torch.autograd.grad(m.MuirChunkFunction.apply(*x, 64)[0].float().sum(), leaves, create_graph=c)
+           for c in (False, True)]
+    assert all(torch.equal(a, b) for a, b in zip(*got))
+    with pytest.raises(RuntimeError, match="differentiated again"):
+        sum((t.float() ** 2).sum() for t in got[1]).backward()
     m.device_wait_status()
