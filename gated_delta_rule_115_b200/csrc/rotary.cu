@@ -12,8 +12,11 @@
 //
 // Angles: p f_i reaches 1e6 turns and more in long contexts, where float32 has no
 // fraction left, so the angle is formed and reduced to a fraction of a turn in
-// float64 (two multiplies, one round, one subtract) and only then rounded to
-// float32 for sincospi: an error below 2^-24 half turns at any int32 position.
+// float64, and only then rounded to float32 for sincospi.  Near position 2^31 even
+// float64 is short: p f, 1 / (2 pi) and their product are each off by 2^-53 of up to
+// 2^28 turns, 2^-22.9 half turns together.  The rests of all three, which fma gives
+// exactly, are therefore added after the reduction: the fraction is off by 2^-54 half
+// turns and its rounding to float32 by 2^-25, at any int32 position.
 //
 // Bound by HBM: q and k are read once and written once (32768 tokens of 16 + 4 heads of 128 in
 // bfloat16: 54 us, 6.2 TB/s).  A block takes a few
@@ -31,6 +34,7 @@ namespace {
 constexpr int kRotThreads = 256;
 constexpr int kRotItems = 2;       // items of two 16-byte vectors in flight per thread
 constexpr int kRotTabPairs = 1024; // (token, pair) entries of the table
+constexpr double kInv2Pi = 0.15915494309189535, kInv2PiRest = -9.839338337591243e-18;  // 1 / (2 pi), their sum
 
 __device__ __forceinline__ void rot_unpack(const uint4& a, float* v, float) {
     v[0] = __uint_as_float(a.x); v[1] = __uint_as_float(a.y);
@@ -117,8 +121,11 @@ __global__ void __launch_bounds__(kRotThreads, 5) k_rotary(RotaryArgs p) {
                 const int t = e / half, i = e - t * half;
                 const long long row = tok0 + t;
                 const int pos = p.positions ? p.positions[row] : (int)(row % p.T);
-                const double turns = (double)pos * p.inv_freq[i] * 0.15915494309189535;
-                const float w = (float)(2.0 * (turns - rint(turns)));  // half turns in [-1, 1]
+                // products that are not contracted into what follows: their rests are taken apart
+                const double x = pos, f = p.inv_freq[i];
+                const double a = __dmul_rn(x, f), turns = __dmul_rn(a, kInv2Pi);
+                const double rest = fma(a, kInv2Pi, -turns) + fma(a, kInv2PiRest, fma(x, f, -a) * kInv2Pi);
+                const float w = (float)(2.0 * (turns - rint(turns) + rest));  // half turns in [-1, 1]
                 float sn, cs;
                 sincospif(w, &sn, &cs);
                 const int at = (t * (2 * Q) + (i % V) / 4) * rot_items + i / V;

@@ -386,7 +386,8 @@ muir_status muir_qk_prologue_bwd(long long rows, int d, muir_dtype dtype, const 
  *                 must not otherwise overlap them
  *   positions   : device int32 [B][T], or NULL = the token's index 0 .. T-1
  *   inv_freq    : device float64 [rot/2], radians per position.  Angles are formed
- *                 and reduced in float64: exact to float32 rounding at any position
+ *                 and reduced in float64 with the rests of their products: exact to
+ *                 float32 rounding (2^-25 half turns) at any position
  *   rot         : a multiple of 16, 16 <= rot <= d; channels past it pass through
  * d is 64 or 128, leading dimensions are multiples of 16 bytes (8 or 4 elements).
  * B * T = 0 enqueues nothing.  Float32 arithmetic, rounded once to dtype.

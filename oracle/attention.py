@@ -10,11 +10,29 @@ import math
 import numpy as np
 
 
+_PI = 314159265358979323846264338327950288419716939937510  # 10^50 pi
+
+
+def angles(positions, inv_freq):
+    """[..., rot / 2]: position times frequency (the float64 value as it stands), reduced to
+    [-pi, pi].  Product and reduction in whole numbers: in float64 they are off by 2^-53 of
+    the angle, which at positions near 2^31 is more than the kernel's own rounding."""
+    p, one = np.asarray(positions).astype(object), 1 << 200
+    turn = one * 10 ** 50 // (2 * _PI)
+    out = np.empty(p.shape + (len(inv_freq),))
+    for i, f in enumerate(inv_freq):
+        m, e = math.frexp(float(f))
+        x = p * (int(m * 2.0 ** 53) * turn)
+        x = x * 2 ** (e - 53) if e > 53 else x // 2 ** (53 - e)
+        out[..., i] = ((x + one // 2) % one - one // 2) / one * (2 * math.pi)
+    return out
+
+
 def rotary(x, positions, inv_freq, interleaved=False, mscale=1.0, inverse=False):
     """x [B, T, H, d] -> rotated, float64."""
     x = np.asarray(x, np.float64)
     half = len(inv_freq)
-    t = np.asarray(positions, np.float64)[:, :, None] * np.asarray(inv_freq, np.float64)
+    t = angles(positions, inv_freq)
     c, s = mscale * np.cos(t)[:, :, None], mscale * np.sin(t)[:, :, None]
     if inverse:
         s = -s

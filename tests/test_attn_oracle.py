@@ -98,3 +98,20 @@ def test_append_and_step_agree_with_plain_attention():
     for window in (0, 7):
         o, _ = A.attn_step(q, *pages, *scales, table, [40], window=window)
         assert np.allclose(o, A.attention(q, k[0], v[0], True, window)["o"])
+
+
+def test_angles_are_reduced_exactly():
+    """Against rational arithmetic with more digits of pi, and plain float64 where that is exact
+    enough."""
+    from fractions import Fraction
+    pi = Fraction(3141592653589793238462643383279502884197169399375105820974944592307816406286, 10 ** 75)
+    f = [1.0, 0.8659643233600653, 1e-4, 3.0, 2.0 ** 60, 0.0]
+    p = np.array([[0, 1, -7], [2 ** 31 - 1, 2097695146, 12345]])
+    got = A.angles(p, f)
+    for i, j in np.ndindex(p.shape):
+        for n, x in enumerate(f):
+            t = Fraction(int(p[i, j])) * Fraction(x) / (2 * pi)
+            assert abs(got[i, j, n] - float((t - round(t)) * 2 * pi)) < 1e-15 * 4
+    small = np.random.default_rng(1).integers(0, 1000, (4, 5))
+    t = small[..., None] * np.array([1.0, 0.1])
+    assert np.allclose(np.cos(A.angles(small, [1.0, 0.1])), np.cos(t), atol=1e-12)

@@ -102,3 +102,20 @@ def test_empty_and_other_stream(m):
         y = m.rotary(x, inv_freq=f)
     s.synchronize()
     assert torch.equal(y, want)
+
+
+@pytest.mark.parametrize("base", [0, 2 ** 20, 2 ** 30, -2 ** 31])
+def test_angles_at_any_position(m, base):
+    """Rows (1, 0) give cosine and sine themselves.  The reduced angle, in half turns within
+    [-1, 1], is rounded to float32 once (2^-25 half turns: 9.4e-8), sincospi is within 2 ulp
+    (2^-23: 1.2e-7), products with 1 and 0 are exact: 2.2e-7 at any position.  (An angle formed
+    and reduced in float64 alone is off by up to 2^-22.9 half turns, 4e-7, from 2^30 on.)"""
+    T = 4000
+    pos = torch.randint(0, 2 ** 30 if base < 0 else max(base, 4096), (1, T), generator=torch.Generator().manual_seed(5)) + base
+    f = torch.tensor([1.0, 0.8659643233600653, 0.99, 0.75, 0.5, 0.1, 1e-3, 0.95], dtype=torch.float64)
+    x = torch.zeros(1, T, 1, 64)
+    x[..., :8] = 1.0
+    y = m.rotary(x.cuda(), positions=pos.to(torch.int32).cuda(), inv_freq=f.cuda()).double().cpu().numpy()
+    t = A.angles(pos.numpy(), f.numpy())[:, :, None]
+    assert np.abs(y[..., :8] - np.cos(t)).max() <= 2.2e-7
+    assert np.abs(y[..., 8:16] - np.sin(t)).max() <= 2.2e-7
