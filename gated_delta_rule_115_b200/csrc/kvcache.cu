@@ -399,7 +399,7 @@ __global__ void __launch_bounds__(kStepThreads, HT == 1 ? 2 : 1) k_attn_step(con
         // query fragments of head 8 h + g: step s of the contraction takes channels
         // c * D/4 + 4 s .. + 3 of lane c
         uint32_t qb[HT][KSTEPS][2];
-        float qscale[HT][2];
+        float qscale[HT][2], qrest[HT][2];  // scale log2(e) / (s1 s2) in two factors
 #pragma unroll
         for (int h = 0; h < HT; ++h) {
             const int head = g0 + 8 * h + g;
@@ -422,9 +422,14 @@ __global__ void __launch_bounds__(kStepThreads, HT == 1 ? 2 : 1) k_attn_step(con
             if (mx > 0.f && mx <= 3.4e38f) frexpf(mx, &e);
             const int sh = 14 - e;  // in [-114, 163]: applied in two halves
             const float s1 = ldexpf(1.f, sh / 2), s2 = ldexpf(1.f, sh - sh / 2);
-            const float qs = p.scale_log2 / s1 / s2;
+            // the key's scale is multiplied between the two: queries near 2^-130 over keys near
+            // 2^127 have ordinary scores, but their own factor alone would be subnormal
+            const float qs = p.scale_log2 / s1, qr = 1.f / s2;
 #pragma unroll
-            for (int i = 0; i < 2; ++i) qscale[h][i] = __shfl_sync(0xffffffffu, qs, 4 * (2 * c + i));
+            for (int i = 0; i < 2; ++i) {
+                qscale[h][i] = __shfl_sync(0xffffffffu, qs, 4 * (2 * c + i));
+                qrest[h][i] = __shfl_sync(0xffffffffu, qr, 4 * (2 * c + i));
+            }
 #pragma unroll
             for (int s = 0; s < KSTEPS; ++s)
 #pragma unroll
@@ -482,7 +487,7 @@ __global__ void __launch_bounds__(kStepThreads, HT == 1 ? 2 : 1) k_attn_step(con
                     for (int i = 0; i < 2; ++i)
 #pragma unroll
                         for (int u = 0; u < kU; ++u) {
-                            const float f = qscale[h][i] * mt[u].ks;
+                            const float f = qscale[h][i] * mt[u].ks * qrest[h][i];
 #pragma unroll
                             for (int r = 0; r < 2; ++r) {
                                 float& x = s[u][h][2 * r + i];

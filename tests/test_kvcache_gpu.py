@@ -254,3 +254,19 @@ def test_step_captured_twice(m, lens):
     torch.cuda.synchronize()
     for o, q in zip(outs, qs):
         check(o, q, code, scales, table, ln)
+
+
+@pytest.mark.parametrize("d,Hq", [(64, 2), (128, 16)])
+def test_step_small_queries_over_large_keys(m, d, Hq):
+    """Queries of subnormal size over pages near the largest scale: their scores are ordinary,
+    and the factor between them and the products must not pass through a subnormal."""
+    code, (ks, vs), table, lens = filled(3, 300, 1, d, 32, 31)
+    r = np.random.default_rng(32)
+    sign = r.choice([-1.0, 1.0], d)
+    k = r.uniform(100, 448, code[0].shape) * np.where(r.random(code[0].shape) < r.random((*code[0].shape[:3], 1)), sign, -sign)
+    code[0] = np.where(code[0] & 0x7f == 0x7f, code[0], A.e4m3_encode(k))
+    scales = (np.full_like(ks, 2.0 ** 119), vs)
+    q = torch.from_numpy(sign * r.integers(17, 32, (3, Hq, d)) * 2.0 ** -133).to(torch.bfloat16)
+    top = np.abs(A.e4m3_decode(code[0][table[0, 0], 0, :16]) * 2.0 ** 119 @ q[0].double().numpy().T).max() * d ** -0.5
+    assert 0.5 < top < 16
+    check(step(m, q, code, scales, table, lens), q, code, scales, table, lens)
