@@ -689,16 +689,22 @@ cudaError_t launch_kv_append(const AppendArgs& a, int B, int d, bool bf16, cudaS
 // Query heads of a block: 8 columns of the products, or 16 where the group has more.
 static int step_heads(int Hq, int Hk) { return Hq / Hk <= 8 ? 8 : kMaxRows; }
 
-int attn_step_splits(int B, int Hq, int Hk, int page, int max_pages) {
+int attn_step_splits(int B, int Hq, int Hk, int d, int page, int max_pages) {
     const int per = step_heads(Hq, Hk);
     const long long units = (long long)B * Hk * ((Hq / Hk + per - 1) / per);
     const long long cap = (long long)page * max_pages;
-    // As many blocks as are resident on 148 SMs, two each (one more starts a second round: 2
-    // streams of 8192 tokens and 8 key heads 15.7 us at 19 splits, 12.3 at 16), and none longer
-    // than 2048 keys, so that one long sequence of a ragged batch does not run on after the
-    // others, nor shorter than 256, where a block is mostly its start (4097 tokens of one
-    // stream, 4 key heads: 7.8 us at 256 keys, 8.9 at 512).
-    long long s = 2 * 148 / units;
+    // As many blocks as are resident on 148 SMs, where one more starts a second round: two each (2
+    // streams of 8192 tokens and 8 key heads 15.7 us at 19 splits, 12.3 at 16), one with 16 heads
+    // of 128 channels, whose 215 registers a thread fill an SM (8 streams of 8192 tokens, 16 heads
+    // over 1: 17.9 us at 37 splits, 12.6 at 18; at d = 64, with room for two, 10.0 and 10.4).
+    // None longer than 2048 keys, up to kMaxSplits, so that one long sequence of a ragged batch
+    // does not run on after the others, nor shorter than 256, where a block is mostly its start
+    // (4097 tokens of one stream, 4 key heads: 7.8 us at 256 keys, 8.9 at 512).
+    // All this of the page table's width: the lengths are on the device.  A table much wider
+    // than the sequences costs blocks of fewer keys and empty ones (64 streams of 8192 tokens, 16
+    // heads over 4: 100 us with a table for 16384 tokens, 243 for 131072; of 500: 9.2 for 512, 156).
+    const int resident = d == 128 && per == kMaxRows ? 1 : 2;
+    long long s = resident * 148 / units;
     const long long by_len = (cap + 2047) / 2048;
     if (s < by_len) s = by_len;
     const long long most = (cap + 255) / 256;
@@ -708,7 +714,7 @@ int attn_step_splits(int B, int Hq, int Hk, int page, int max_pages) {
 }
 
 size_t attn_step_ws_bytes(int B, int Hq, int Hk, int d, int page, int max_pages) {
-    const size_t s = attn_step_splits(B, Hq, Hk, page, max_pages);
+    const size_t s = attn_step_splits(B, Hq, Hk, d, page, max_pages);
     return s == 1 ? 0 : (size_t)B * Hq * s * (d + 1) * 4;
 }
 
@@ -722,7 +728,7 @@ static cudaError_t step(const StepArgs& a, dim3 grid, cudaStream_t st) {
 }
 
 cudaError_t launch_attn_step(StepArgs a, int B, int d, void* ws, cudaStream_t st) {
-    a.splits = attn_step_splits(B, a.Hq, a.Hk, a.page, a.max_pages);
+    a.splits = attn_step_splits(B, a.Hq, a.Hk, d, a.page, a.max_pages);
     a.min_keys = 256;
     a.part = static_cast<float*>(ws);
     a.part_lse = a.part + (size_t)B * a.Hq * a.splits * d;

@@ -207,3 +207,16 @@ def test_scales_that_leave_float32_in_base_two(m):
     """The kernels take scale log2(e): past 2.35e38 that is no float32 any more."""
     assert attn(m, scale=2.4e38) == attn(m, True, scale=2.4e38) == INVALID
     assert step(m, cache(m), scale=2.4e38) == step(m, cache(m), scale=-2.4e38) == INVALID
+
+
+@pytest.mark.parametrize("d,Hq,Hk,resident", [(128, 16, 4, 296), (64, 16, 4, 296), (64, 16, 1, 296), (128, 16, 1, 148),
+                                              (128, 64, 4, 148)])
+@pytest.mark.parametrize("B", [1, 2, 8])
+def test_step_splits_fill_one_round(m, B, d, Hq, Hk, resident):
+    """Sequences are split into as many blocks as the kernel has resident on 148 SMs (two each;
+    one with 16 heads of 128 channels a block), as long as that leaves 256 tokens or more."""
+    tokens = 16384
+    c = cache(m, Hk=Hk, d=d, page=64, max_pages=tokens // 64)
+    splits = m.lib().muir_attn_step_workspace(B, Hq, ctypes.byref(c)) // (B * Hq * (d + 1) * 4)
+    units = B * Hk * -(-Hq // Hk // 16)
+    assert splits == max(tokens // 2048, min(resident // units, tokens // 256))

@@ -270,3 +270,18 @@ def test_step_small_queries_over_large_keys(m, d, Hq):
     top = np.abs(A.e4m3_decode(code[0][table[0, 0], 0, :16]) * 2.0 ** 119 @ q[0].double().numpy().T).max() * d ** -0.5
     assert 0.5 < top < 16
     check(step(m, q, code, scales, table, lens), q, code, scales, table, lens)
+
+
+@pytest.mark.parametrize("B,most,Hq,Hk,d,page,wide", [(3, 700, 16, 4, 128, 64, 40000), (4, 300, 16, 1, 128, 16, 9000),
+                                                     (2, 257, 24, 1, 64, 32, 300000), (8, 5000, 32, 2, 128, 64, 8192)])
+def test_step_with_a_table_wider_than_the_sequences(m, B, most, Hq, Hk, d, page, wide):
+    """As a server allocates it: room for a context limit that no sequence has reached; the
+    entries behind a sequence name no page, or pages of others."""
+    code, scales, table, lens = filled(B, most, Hk, d, page, 41)
+    q = torch.randn(B, Hq, d, generator=torch.Generator().manual_seed(42)).to(torch.bfloat16)
+    full = np.full((B, wide // page), -1, np.int32)
+    full[:, : table.shape[1]] = table
+    full[1, table.shape[1]:] = table[0, 0]
+    for window in (0, 100):
+        check(step(m, q, code, scales, full, lens, window=window), q, code, scales, full, lens, window=window)
+    m.device_wait_status()
