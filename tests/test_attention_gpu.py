@@ -338,3 +338,42 @@ def test_windows_that_look_ahead(m, B, Tq, Tk, Hq, Hk, d, window):
         check_bwd({n: t[b] for n, t in g.items()}, r, own_o=True)
     if window == 1:
         assert not g["dq"][:, -1].any()
+
+
+@pytest.mark.parametrize("d,causal,window", [(64, True, 0), (128, True, 5), (64, False, 0), (128, True, 40)])
+def test_ragged_sequences_of_several_launches(m, d, causal, window):
+    """300 sequences of their own lengths, each against the oracle: what a later launch takes
+    from its place in the list (offsets, order of blocks, rows of few keys) is its own."""
+    r = np.random.default_rng(d + window)
+    lens = r.integers(0, 40, 300)
+    lens_k = np.where(r.random(300) < 0.5, lens, r.integers(0, 60, 300))
+    for i, (a, b) in {0: (1, 1), 5: (300, 300), 127: (9, 9), 128: (140, 141), 255: (3, 7), 256: (1, 30), 299: (17, 17)}.items():
+        lens[i], lens_k[i] = a, b
+    cu, sq = spans(lens)
+    ck, sk = spans(lens_k)
+    q, k, v, do = (rnd(1, T, H, d, seed=s) for T, H, s in ((cu[-1], 4, 1), (ck[-1], 2, 2), (ck[-1], 2, 3), (cu[-1], 4, 4)))
+    args = dict(cu_seqlens=cu, cu_seqlens_k=ck, causal=causal, window=window)
+    dev = [t.cuda() for t in (q, k, v, do)]
+    o, lse = m.attn_fwd_varlen(*dev[:3], **args)
+    g = m.attn_bwd_varlen(*dev[:3], o, lse, dev[3], **args)
+    m.device_wait_status()
+    for a, b, res in zip(sq, sk, oracle(q, k, v, do, list(zip(sq, sk)), causal=causal, window=window)):
+        check_fwd(o[a], lse[0, :, a[1]], res)
+        check_bwd({"dq": g["dq"][a], "dk": g["dk"][b], "dv": g["dv"][b]}, res, own_o=True)
+
+
+@pytest.mark.parametrize("d,Hq,Hk", [(64, 16, 4), (128, 8, 8)])
+def test_every_one_of_many_launches(m, d, Hq, Hk):
+    """Each of hundreds of results is compared, on the device, not the last one alone."""
+    q, do = (rnd(3, 513, Hq, d, seed=s).cuda() for s in (1, 4))
+    k, v = (rnd(3, 513, Hk, d, seed=s).cuda() for s in (2, 3))
+    o, lse = m.attn_fwd(q, k, v)
+    g = m.attn_bwd(q, k, v, o, lse, do)
+    differ = torch.zeros(5, dtype=torch.int64, device="cuda")
+    for _ in range(400):
+        o2, lse2 = m.attn_fwd(q, k, v)
+        g2 = m.attn_bwd(q, k, v, o, lse, do)
+        pairs = [(o, o2), (lse, lse2)] + [(g[n], g2[n]) for n in ("dq", "dk", "dv")]
+        differ += torch.stack([(a != b).any() for a, b in pairs])
+    m.device_wait_status()
+    assert not differ.any(), differ.tolist()
