@@ -197,6 +197,7 @@ constexpr int kU = kWarpKeys / 16;         // a warp's
 constexpr int kMaxRows = 16;               // query heads of a block
 constexpr int kMaxSplits = 128;            // of a sequence; two to a thread of the smallest join
 constexpr float kSlack = 8.f;              // log2 of how far a weight may exceed 1
+constexpr int kMaxQueryExp = 109;          // log2 of a query row's largest factor
 constexpr float kWeightExp = 7.f;          // fp16 weights are 2^(score - reference + 7) <= 2^15
 
 struct StepMeta {        // per group of a stage
@@ -274,7 +275,10 @@ __device__ __forceinline__ uint32_t step_off(int r, int c) {
 // leaves by key and the output product takes by head, are transposed in registers.
 //
 // Query rows are scaled by a power of two to a largest magnitude in [2^13, 2^14): fp16
-// then holds bf16 values exactly down to 2^-28 of the row's largest.  Softmax runs in
+// then holds bf16 values exactly down to 2^-28 of the row's largest.  The power ends at 2^109,
+// under which the smallest bf16 value, 2^-133, is fp16's and all are exact: with more, the
+// factor of the scores of queries near 2^-128 would be subnormal, and lose its bits where a
+// page's scale near 2^120 makes those scores ordinary ones.  Softmax runs in
 // base 2 against references held in float32 that move only when a score outgrows them by
 // 2^8: m over the scores for the normaliser, and M over score + log2(value scale) for the
 // weights of the value codes, which are kept as fp16(2^(score + log2 scale - M + 7)):
@@ -399,7 +403,7 @@ __global__ void __launch_bounds__(kStepThreads, HT == 1 ? 2 : 1) k_attn_step(con
         // query fragments of head 8 h + g: step s of the contraction takes channels
         // c * D/4 + 4 s .. + 3 of lane c
         uint32_t qb[HT][KSTEPS][2];
-        float qscale[HT][2], qrest[HT][2];  // scale log2(e) / (s1 s2) in two factors
+        float qscale[HT][2];
 #pragma unroll
         for (int h = 0; h < HT; ++h) {
             const int head = g0 + 8 * h + g;
@@ -420,16 +424,11 @@ __global__ void __launch_bounds__(kStepThreads, HT == 1 ? 2 : 1) k_attn_step(con
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
             int e = 0;
             if (mx > 0.f && mx <= 3.4e38f) frexpf(mx, &e);
-            const int sh = 14 - e;  // in [-114, 163]: applied in two halves
+            const int sh = min(14 - e, kMaxQueryExp);  // from -114: applied in two halves
             const float s1 = ldexpf(1.f, sh / 2), s2 = ldexpf(1.f, sh - sh / 2);
-            // the key's scale is multiplied between the two: queries near 2^-130 over keys near
-            // 2^127 have ordinary scores, but their own factor alone would be subnormal
-            const float qs = p.scale_log2 / s1, qr = 1.f / s2;
+            const float qs = p.scale_log2 / s1 / s2;
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                qscale[h][i] = __shfl_sync(0xffffffffu, qs, 4 * (2 * c + i));
-                qrest[h][i] = __shfl_sync(0xffffffffu, qr, 4 * (2 * c + i));
-            }
+            for (int i = 0; i < 2; ++i) qscale[h][i] = __shfl_sync(0xffffffffu, qs, 4 * (2 * c + i));
 #pragma unroll
             for (int s = 0; s < KSTEPS; ++s)
 #pragma unroll
@@ -487,7 +486,7 @@ __global__ void __launch_bounds__(kStepThreads, HT == 1 ? 2 : 1) k_attn_step(con
                     for (int i = 0; i < 2; ++i)
 #pragma unroll
                         for (int u = 0; u < kU; ++u) {
-                            const float f = qscale[h][i] * mt[u].ks * qrest[h][i];
+                            const float f = qscale[h][i] * mt[u].ks;
 #pragma unroll
                             for (int r = 0; r < 2; ++r) {
                                 float& x = s[u][h][2 * r + i];
@@ -695,7 +694,7 @@ int attn_step_splits(int B, int Hq, int Hk, int d, int page, int max_pages) {
     const long long cap = (long long)page * max_pages;
     // As many blocks as are resident on 148 SMs, where one more starts a second round: two each (2
     // streams of 8192 tokens and 8 key heads 15.7 us at 19 splits, 12.3 at 16), one with 16 heads
-    // of 128 channels, whose 215 registers a thread fill an SM (8 streams of 8192 tokens, 16 heads
+    // of 128 channels, whose 211 registers a thread fill an SM (8 streams of 8192 tokens, 16 heads
     // over 1: 17.9 us at 37 splits, 12.6 at 18; at d = 64, with room for two, 10.0 and 10.4).
     // None longer than 2048 keys, up to kMaxSplits, so that one long sequence of a ragged batch
     // does not run on after the others, nor shorter than 256, where a block is mostly its start
