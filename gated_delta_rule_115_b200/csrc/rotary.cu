@@ -14,9 +14,9 @@
 // fraction left, so the angle is formed and reduced to a fraction of a turn in
 // float64, and only then rounded to float32 for sincospi.  Near position 2^31 even
 // float64 is short: p f, 1 / (2 pi) and their product are each off by 2^-53 of up to
-// 2^28 turns, 2^-22.9 half turns together.  The rests of all three, which fma gives
-// exactly, are therefore added after the reduction: the fraction is off by 2^-54 half
-// turns and its rounding to float32 by 2^-25, at any int32 position.
+// 2^28 turns, 2^-22.9 half turns together.  The whole turns are therefore taken off the
+// unrounded product, and the rests of p f and of 1 / (2 pi) added: the fraction is off by
+// 2^-53 half turns and its rounding to float32 by 2^-25, at any int32 position.
 //
 // Bound by HBM: q and k are read once and written once (32768 tokens of 16 + 4 heads of 128 in
 // bfloat16: 54 us, 6.2 TB/s).  A block takes a few
@@ -121,11 +121,11 @@ __global__ void __launch_bounds__(kRotThreads, 5) k_rotary(RotaryArgs p) {
                 const int t = e / half, i = e - t * half;
                 const long long row = tok0 + t;
                 const int pos = p.positions ? p.positions[row] : (int)(row % p.T);
-                // products that are not contracted into what follows: their rests are taken apart
+                // a + rest is p f exactly, and fma takes a / (2 pi) less its whole turns unrounded
                 const double x = pos, f = p.inv_freq[i];
-                const double a = __dmul_rn(x, f), turns = __dmul_rn(a, kInv2Pi);
-                const double rest = fma(a, kInv2Pi, -turns) + fma(a, kInv2PiRest, fma(x, f, -a) * kInv2Pi);
-                const float w = (float)(2.0 * (turns - rint(turns) + rest));  // half turns in [-1, 1]
+                const double a = __dmul_rn(x, f), rest = fma(x, f, -a);
+                const double turn = fma(a, kInv2Pi, -rint(__dmul_rn(a, kInv2Pi)));
+                const float w = 2.f * (float)(turn + fma(a, kInv2PiRest, rest * kInv2Pi));  // in [-1, 1]
                 float sn, cs;
                 sincospif(w, &sn, &cs);
                 const int at = (t * (2 * Q) + (i % V) / 4) * rot_items + i / V;
