@@ -623,15 +623,17 @@ def kv_append(k, v, k_pages, v_pages, k_scale, v_scale, page_table, start, count
     """Writes the tokens of ``k, v [B, T, Hk, d]`` (bfloat16 or float32) into the cache
     (:func:`kv_cache`), in place (``muir_kv_append``): token t of sequence b to position
     ``start[b] + t`` for t below ``count[b]`` (None: T).  ``page_table`` is int32
-    ``[B, max_pages]``, ``start`` and ``count`` int32 ``[B]``, all on the device."""
+    ``[B, max_pages]``, ``start`` and ``count`` int32 ``[B]``, all on the device.  The new
+    tokens' entries of the table must not name a page twice."""
     (_nat or _native()).kv_append(k, v, k_pages, v_pages, k_scale, v_scale, page_table, start, count)
 
 
 def attn_step(q, k_pages, v_pages, k_scale, v_scale, page_table, lens, scale=None, window=0,
               o=None, ws=None):
-    """One bfloat16 query token ``q [B, Hq, d]`` of every sequence attends over its first
-    ``lens[b]`` cached tokens, or the last ``window`` of them (``muir_attn_step``).
-    ``scale`` defaults to ``d ** -0.5``.  Returns ``o [B, Hq, d]``."""
+    """One bfloat16 query token of every sequence, ``q [B, Hq, d]`` (contiguous), attends over
+    its first ``lens[b]`` cached tokens, or the last ``window`` of them (``muir_attn_step``).
+    ``scale`` defaults to ``d ** -0.5``.  Work is split by the width of ``page_table``: one
+    much wider than the longest sequence costs time.  Returns ``o [B, Hq, d]``."""
     return (_nat or _native()).attn_step(q, k_pages, v_pages, k_scale, v_scale, page_table, lens, scale,
                                          window, o, ws)
 

@@ -424,7 +424,8 @@ muir_status muir_rotary(int B, int T, int Hq, int Hk, int d, int rot, muir_dtype
  * tensor cores: 4 d flops a visible pair forward, 10 d backward.
  *
  * muir_attn_bwd: gradients of sum(o * dO).  o and lse are the forward's; the
- * probabilities are recomputed from lse.  Workspace: two float32 a query and head.
+ * probabilities are recomputed from lse.  Workspace: two float32 a query and head,
+ * the call's until it has finished.
  *
  * The varlen forms take num_seqs sequences packed in one buffer, as muir_chunk_fwd_varlen
  * does: B = 1, Tq and Tk total tokens, cu_q and cu_k HOST arrays of num_seqs + 1 offsets
@@ -491,7 +492,8 @@ typedef struct {
  * but for codes that become subnormal).  The scale that a page held before its
  * first row is written is ignored.  Infinities are stored as +-448, NaN as NaN.
  * Tokens past max_pages * page are dropped.  Rows behind the new tokens keep what
- * they hold.  No two sequences of one call may write to the same page.
+ * they hold.  Every page that a call writes to must be named once in the table's
+ * entries of the new tokens: not by two sequences, nor twice by one.
  */
 muir_status muir_kv_append(int B, int T, muir_dtype dtype, const void* k, long long k_ld,
                            const void* v, long long v_ld, const muir_kv_cache* cache,
@@ -510,8 +512,12 @@ muir_status muir_kv_append(int B, int T, muir_dtype dtype, const void* k, long l
  * Products in fp16 with float32 sums (the codes are exact in fp16), softmax in
  * float32.  Bound by HBM: the visible codes are read once for up to 16 query heads
  * of a key head.  Work is split over the length; the parts are joined in a fixed
- * order, so results repeat bit for bit.  The workspace (query below; 0 bytes when
- * nothing is split) belongs to the call until it has finished.
+ * order, so results repeat bit for bit.  How many parts goes by the table's
+ * max_pages * page tokens (lens is on the device): a table much wider than the
+ * sequences leaves parts small or empty, which cost time and workspace, so a caller
+ * with a large context limit passes a table as wide as its longest sequence.  The
+ * workspace (query below; 0 bytes when nothing is split) belongs to the call until
+ * it has finished.
  */
 size_t muir_attn_step_workspace(int B, int Hq, const muir_kv_cache* cache);
 muir_status muir_attn_step(int B, int Hq, const muir_kv_cache* cache, const void* q,
