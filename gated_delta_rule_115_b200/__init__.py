@@ -27,7 +27,8 @@ __all__ = [
     "MuirError", "lib", "chunk_fwd", "chunk_bwd", "chunk_fwd_varlen", "chunk_bwd_varlen",
     "recurrent_step", "qk_prologue", "chunk_fwd_fused", "chunk_bwd_fused", "MuirFusion",
     "qk_prologue_bwd", "rotary", "rotary_frequencies", "attn_fwd", "attn_bwd",
-    "attn_fwd_varlen", "attn_bwd_varlen", "MuirRotaryFunction", "MuirAttentionFunction", "kv_cache", "kv_append", "attn_step",
+    "attn_fwd_varlen", "attn_bwd_varlen", "MuirRotaryFunction", "MuirAttentionFunction",
+    "kv_cache", "kv_append", "attn_step",
     "fwd_workspace_bytes", "bwd_workspace_bytes", "MuirChunkFunction",
     "LIB_PATH",
 ]
@@ -684,7 +685,8 @@ class MuirRotaryFunction(torch.autograd.Function):
     call with ``inverse`` turned over, and differentiable in its turn.
 
     ``inplace`` writes over ``q`` and ``k``.  Autograd takes neither leaves for that, nor views
-    in a call that returns two tensors: parts of one projection are rotated in a call each."""
+    in a call that returns two tensors: parts of one projection, as slices of it, are rotated in
+    a call each.  (Pieces from ``split`` or ``unbind`` it refuses too, once they are written.)"""
 
     @staticmethod
     def forward(ctx, q, k=None, positions=None, inv_freq=None, interleaved=False, mscale=1.0, inverse=False,
@@ -695,7 +697,7 @@ class MuirRotaryFunction(torch.autograd.Function):
         if not inplace:
             return rotary(q, k, positions, inv_freq, interleaved, mscale, inverse)
         both = (q,) if k is None else (q, k)
-        if any(ctx.needs_input_grad[:2]):  # what autograd itself refuses, before anything is written
+        if any(ctx.needs_input_grad[:2]):  # autograd would refuse these after they are written
             if any(t.is_leaf and t.requires_grad for t in both):
                 raise ValueError("a leaf that requires a gradient cannot be rotated in place")
             if len(both) > 1 and any(t._is_view() for t in both):
