@@ -307,3 +307,52 @@ def test_chunk_gradients_with_create_graph(m, state):
     with pytest.raises(RuntimeError, match="differentiated again"):
         sum((t.float() ** 2).sum() for t in got[1]).backward()
     m.device_wait_status()
+
+
+@pytest.mark.gpu
+def test_captured_training_pass(m):
+    """Rotation, attention and both backward passes in one graph, replayed on new values."""
+    T, Hq, Hk, d = 200, 4, 2, 64
+    f, s = m.rotary_frequencies(d)
+    x = rnd(1, T, (Hq + 2 * Hk) * d, seed=1).cuda().requires_grad_()
+    do = rnd(1, T, Hq, d, seed=2).cuda()
+
+    def one():
+        p = x * 1
+        q, k, v = (p[..., a * d: b * d].unflatten(-1, (b - a, d)) for a, b in ((0, Hq), (Hq, Hq + Hk), (Hq + Hk, Hq + 2 * Hk)))
+        q, k = (m.MuirRotaryFunction.apply(t, None, None, f, False, s, False, True) for t in (q, k))
+        return torch.autograd.grad(m.MuirAttentionFunction.apply(q, k, v, True, 70, None, [0, 77, T]), x, do)[0]
+
+    stream = torch.cuda.Stream()
+    stream.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(stream):
+        one()
+    torch.cuda.current_stream().wait_stream(stream)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = one()
+    for seed in (3, 4):
+        with torch.no_grad():
+            x.copy_(rnd(*x.shape, seed=seed))
+            do.copy_(rnd(*do.shape, seed=seed + 10))
+        graph.replay()
+        assert torch.equal(got, one())
+    m.device_wait_status()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("B,Tq,Tk", [(0, 5, 5), (2, 0, 7), (2, 7, 0), (1, 0, 0), (3, 1, 1)])
+def test_gradients_of_empty_calls(m, B, Tq, Tk):
+    """No sequences, no queries, no keys: shapes kept, zeros where nothing is seen."""
+    q, k, v = (rnd(B, T, H, 64, seed=T + H).cuda().requires_grad_() for T, H in ((Tq, 4), (Tk, 2), (Tk, 2)))
+    f, _ = m.rotary_frequencies(64)
+    qr, kr = m.MuirRotaryFunction.apply(q, None, None, f), m.MuirRotaryFunction.apply(k, None, None, f)
+    o = m.MuirAttentionFunction.apply(qr, kr, v)
+    o.sum().backward()
+    assert [t.grad.shape for t in (q, k, v)] == [t.shape for t in (q, k, v)] and o.shape == q.shape
+    if Tq != 1:
+        assert not o.any() and not any(t.grad.any() for t in (q, k, v))
+    else:
+        assert torch.equal(o, v.repeat_interleave(2, 2)) and not q.grad.any() and not k.grad.any()
+        assert (v.grad == 2).all()
+    m.device_wait_status()
